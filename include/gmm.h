@@ -56,7 +56,8 @@ typedef enum {
   GMM_I4 = 7,        /* two's-complement int4, two to a byte (element i in the low
                         nibble of byte i/2 when i is even, the high nibble when odd) */
   GMM_U4 = 8,        /* unsigned int4, packed as GMM_I4 */
-  GMM_F4E2M1 = 9     /* OCP fp4 e2m1 (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6), packed as GMM_I4 */
+  GMM_F4E2M1 = 9,    /* OCP fp4 e2m1 (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6), packed as GMM_I4 */
+  GMM_I64 = 10       /* int64 (expert ids only, gmm_moe.h) */
 } gmm_dtype;
 
 typedef enum {
@@ -146,6 +147,12 @@ const char* gmm_last_error(const gmm_handle* h);
  *                scaled f8f6f4 matrix instruction itself, for any pair of
  *                F8E4M3FN / F8E5M2 / F4E2M1 operands.  Byte 255 (NaN in the
  *                microscaling encoding) is outside the contract.
+ *                (BF16, F4E2M1) takes an E8M0 rhs_scale too (no lhs_scale):
+ *                microscaled fp4 weights as gmm_quant_mxfp4_run of gmm_moe.h
+ *                writes them, widened to bf16 with their scale.  Weights
+ *                below the smallest normal bf16 (bytes 0 and 1) may count as
+ *                zero, and those past the largest (bytes 253 and 254) become
+ *                infinities; byte 255 makes its block NaN.
  *   group_offset NULL (s = 0) or a device pointer to one int32 s.
  *   out          [M,N], F32 or BF16.  All M rows are written.  out must not
  *                overlap any input.

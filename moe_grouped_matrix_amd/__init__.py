@@ -8,7 +8,10 @@ from ._binding import (EXPORTED, FLAG_BAD_OFFSET, FLAG_NEGATIVE_SIZE, FLAG_SCHED
                        LIB_PATH, GmmDeviceDataError, GmmError, GmmInvalid, GmmUnsupported,
                        debug_worklist, device_flags, gmm, handle, load, quant_fp8, set_grid_limit,
                        set_tile_policy, tgmm, widen_scales)
+from ._moe import (EXPORTED_MOE, FLAG_BAD_ROW, combine, combine_grad, dispatch, quant_mxfp4,  # noqa: F401
+                   sort_tokens, widen_mxfp4)
 
-__all__ = ["gmm", "tgmm", "quant_fp8", "widen_scales", "device_flags", "debug_worklist", "set_tile_policy",
+__all__ = ["gmm", "tgmm", "quant_fp8", "widen_scales", "sort_tokens", "dispatch", "combine", "combine_grad",
+           "quant_mxfp4", "widen_mxfp4", "device_flags", "debug_worklist", "set_tile_policy",
            "set_grid_limit", "load", "handle", "GmmError", "GmmInvalid", "GmmUnsupported", "GmmDeviceDataError",
            "LIB_PATH"]

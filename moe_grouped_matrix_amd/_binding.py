@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libgmm.so")
 
 GMM_F32, GMM_BF16, GMM_F8E4M3FN, GMM_I32, GMM_F8E5M2, GMM_E8M0, GMM_I8 = 0, 1, 2, 3, 4, 5, 6
 GMM_I4, GMM_U4, GMM_F4E2M1 = 7, 8, 9
+GMM_I64 = 10  # expert ids only
 # four-bit weights: packed bytes (uint8, or float4_e2m1fn_x2) named by format
 PACKED_FORMATS = {"int4": GMM_I4, "uint4": GMM_U4, "fp4_e2m1": GMM_F4E2M1}
 GMM_OK, GMM_E_INVALID, GMM_E_UNSUPPORTED, GMM_E_HIP, GMM_E_DEVICE_DATA = 0, -1, -2, -3, -4
@@ -98,6 +99,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gmm_set_grid_limit.restype = ctypes.c_int
             lib.gmm_debug_worklist.argtypes = [vp, tp, vp, i64, i64, i32, vp, i64, vp, vp]
             lib.gmm_debug_worklist.restype = ctypes.c_int
+            sz = ctypes.c_size_t
+            lib.gmm_sort_tokens_workspace.argtypes = [i64, i64, ctypes.POINTER(sz)]
+            lib.gmm_sort_tokens_workspace.restype = ctypes.c_int
+            lib.gmm_sort_tokens_run.argtypes = [vp, tp, tp, tp, vp, sz, vp]
+            lib.gmm_sort_tokens_run.restype = ctypes.c_int
+            lib.gmm_dispatch_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_dispatch_run.restype = ctypes.c_int
+            lib.gmm_combine_run.argtypes = [vp, tp, tp, tp, tp, vp]
+            lib.gmm_combine_run.restype = ctypes.c_int
+            lib.gmm_combine_grad_run.argtypes = [vp, tp, tp, tp, tp, tp, tp, vp]
+            lib.gmm_combine_grad_run.restype = ctypes.c_int
+            lib.gmm_quant_mxfp4_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_quant_mxfp4_run.restype = ctypes.c_int
+            lib.gmm_widen_mxfp4_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_widen_mxfp4_run.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -130,20 +146,20 @@ def handle(device: Union[int, torch.device, None] = None):
     return h
 
 
-def _view(t: Optional[torch.Tensor], name: str):
+def _view(t: Optional[torch.Tensor], name: str, dtypes=_DTYPE):
     if t is None:
         return None
     if not t.is_cuda:
         raise GmmInvalid(GMM_E_INVALID, f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise GmmInvalid(GMM_E_INVALID, f"{name} must be contiguous")
-    if t.dtype not in _DTYPE:
+    if t.dtype not in dtypes:
         raise GmmInvalid(GMM_E_INVALID, f"{name}: unsupported dtype {t.dtype}")
     if t.dim() > 4:
         raise GmmInvalid(GMM_E_INVALID, f"{name}: more than 4 dimensions")
     v = GmmTensor()
     v.data = t.data_ptr() if t.numel() else None
-    v.dtype = _DTYPE[t.dtype]
+    v.dtype = dtypes[t.dtype]
     v.ndim = t.dim()
     for i, s in enumerate(t.shape):
         v.shape[i] = s

@@ -14,7 +14,11 @@
 #include <string>
 
 #include "gmm.h"
+#include "gmm_handle.hpp"
 #include "gmm_launch.hpp"
+#include "gmm_tensor.hpp"
+
+using namespace gmmh;
 
 constexpr size_t kDeviceBlock = 16;  // the data-error flag word
 static_assert(gmmk::kFlagNegative == GMM_FLAG_NEGATIVE_SIZE && gmmk::kFlagExceed == GMM_FLAG_SIZES_EXCEED_M &&
@@ -22,92 +26,10 @@ static_assert(gmmk::kFlagNegative == GMM_FLAG_NEGATIVE_SIZE && gmmk::kFlagExceed
               "the kernels' flag bits are the header's");
 constexpr size_t kQueueBlock = gmmk::kQueueWords * sizeof(int32_t);
 
-struct gmm_handle {
-  int device = 0;
-  int cu_count = 0;
-  uint32_t* flags = nullptr;  // device word of data-error flags (kDeviceBlock bytes)
-  // the transposed product's work-queue counters (kQueueWords int32, zero
-  // between calls), one block per stream: calls on one stream run in order,
-  // so each call finds its stream's counters reset by the previous one;
-  // calls on different streams never share counters
-  std::map<void*, int32_t*> queues;
-  int tile_policy = 0;        // 0 auto, 1 small tiles, 2 big tiles
-  int grid_limit = 0;         // > 0: at most this many workgroups per launch
-  void* scratch = nullptr;    // device address of the device's static scratch
-  std::string err;
-};
-
 // Device addresses of the static scratch (gmmk::static_scratch_address), one
 // per device, looked up by the first gmm_create on that device.
 static std::mutex g_scratch_mu;
 static std::map<int, void*> g_scratch;
-
-namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) (void)hipSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
-gmm_status fail(gmm_handle* h, gmm_status st, const std::string& msg) {
-  if (h) h->err = msg;
-  return st;
-}
-
-std::string shape_str(const gmm_tensor* t) {
-  std::string s = "(";
-  for (int i = 0; i < t->ndim && i < 4; ++i) {
-    if (i) s += ",";
-    s += std::to_string(t->shape[i]);
-  }
-  return s + ")";
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_size(int dtype) {
-  switch (dtype) {
-    case GMM_F32: return 4;
-    case GMM_BF16: return 2;
-    case GMM_F8E4M3FN: return 1;
-    case GMM_F8E5M2: return 1;
-    case GMM_E8M0: return 1;
-    case GMM_I8: return 1;
-    case GMM_I32: return 4;
-    default: return 0;
-  }
-}
-
-long long numel(const gmm_tensor* t) {
-  long long n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
-}
-
-bool four_bit(int dtype) { return dtype == GMM_I4 || dtype == GMM_U4 || dtype == GMM_F4E2M1; }
-
-// bytes of a tensor's data (four-bit types: two elements to a byte)
-long long tensor_bytes(const gmm_tensor* t) {
-  return four_bit(t->dtype) ? (numel(t) + 1) / 2 : numel(t) * elem_size(t->dtype);
-}
-
-bool overlaps(const gmm_tensor* a, const gmm_tensor* b) {
-  if (!a || !b || !a->data || !b->data) return false;
-  const char* a0 = static_cast<const char*>(a->data);
-  const char* b0 = static_cast<const char*>(b->data);
-  const char* a1 = a0 + tensor_bytes(a);
-  const char* b1 = b0 + tensor_bytes(b);
-  return a0 < b1 && b0 < a1;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -241,7 +163,7 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
     kc.fmt = f8_code(ld) | f8_code(rd) << 3;
   } else {
     const bool known_l = elem_size(ld) > 0 || four_bit(ld), known_r = elem_size(rd) > 0 || four_bit(rd);
-    if (!known_l || !known_r || ld == GMM_I32 || rd == GMM_I32 || ld == GMM_E8M0 || rd == GMM_E8M0)
+    if (!known_l || !known_r || ld == GMM_I32 || rd == GMM_I32 || ld == GMM_I64 || rd == GMM_I64 || ld == GMM_E8M0 || rd == GMM_E8M0)
       return fail(h, GMM_E_INVALID, "unsupported lhs / rhs dtype");
     return fail(h, GMM_E_UNSUPPORTED, "unsupported (lhs, rhs) dtype pair");
   }
@@ -279,8 +201,11 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
   kc.scaled = !mx && (rhs_scale != nullptr || lhs_scale != nullptr);
   kc.mx = mx;
   if (mx) {
-    if (kc.op != gmmk::Op::FP8)
-      return fail(h, GMM_E_UNSUPPORTED, "E8M0 block scales need e4m3fn, e5m2 or fp4 e2m1 operands on both sides");
+    const bool weight_only = kc.op == gmmk::Op::BF16 && rd == GMM_F4E2M1;
+    if (kc.op != gmmk::Op::FP8 && !weight_only)
+      return fail(h, GMM_E_UNSUPPORTED,
+                  "E8M0 block scales need e4m3fn, e5m2 or fp4 e2m1 operands on both sides, or bf16 lhs and fp4 e2m1 rhs");
+    if (weight_only && lhs_scale) return fail(h, GMM_E_UNSUPPORTED, "a bf16 lhs takes no E8M0 lhs_scale");
     if (K != 32 * nb) return fail(h, GMM_E_UNSUPPORTED, "E8M0 block scales cover blocks of 32 K elements (nb = K/32)");
   }
 
@@ -475,7 +400,8 @@ static gmm_status run_tgmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tenso
   if (out->shape[1] != K || out->shape[2] != N)
     return fail(h, GMM_E_INVALID, "out must be [Ga," + std::to_string(K) + "," + std::to_string(N) + "], got " + shape_str(out));
   if (lhs->dtype != GMM_BF16 || rhs->dtype != GMM_BF16) {
-    if (elem_size(lhs->dtype) == 0 || elem_size(rhs->dtype) == 0 || lhs->dtype == GMM_I32 || rhs->dtype == GMM_I32)
+    if (elem_size(lhs->dtype) == 0 || elem_size(rhs->dtype) == 0 || lhs->dtype == GMM_I32 || rhs->dtype == GMM_I32 ||
+        lhs->dtype == GMM_I64 || rhs->dtype == GMM_I64)
       return fail(h, GMM_E_INVALID, "unsupported lhs / rhs dtype");
     return fail(h, GMM_E_UNSUPPORTED, "tgmm takes bf16 lhs and rhs");
   }

@@ -102,17 +102,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             sz = ctypes.c_size_t
             lib.gmm_sort_tokens_workspace.argtypes = [i64, i64, ctypes.POINTER(sz)]
             lib.gmm_sort_tokens_workspace.restype = ctypes.c_int
-            lib.gmm_sort_tokens_run.argtypes = [vp, tp, tp, tp, vp, sz, vp]
+            # these take each gmm_tensor as the bytes of the struct (_moe.py)
+            lib.gmm_sort_tokens_run.argtypes = [vp, vp, vp, vp, vp, sz, vp]
             lib.gmm_sort_tokens_run.restype = ctypes.c_int
-            lib.gmm_dispatch_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_dispatch_run.argtypes = [vp, vp, vp, vp, vp]
             lib.gmm_dispatch_run.restype = ctypes.c_int
-            lib.gmm_combine_run.argtypes = [vp, tp, tp, tp, tp, vp]
+            lib.gmm_combine_run.argtypes = [vp, vp, vp, vp, vp, vp]
             lib.gmm_combine_run.restype = ctypes.c_int
-            lib.gmm_combine_grad_run.argtypes = [vp, tp, tp, tp, tp, tp, tp, vp]
+            lib.gmm_combine_grad_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
             lib.gmm_combine_grad_run.restype = ctypes.c_int
-            lib.gmm_quant_mxfp4_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_quant_mxfp4_run.argtypes = [vp, vp, vp, vp, vp]
             lib.gmm_quant_mxfp4_run.restype = ctypes.c_int
-            lib.gmm_widen_mxfp4_run.argtypes = [vp, tp, tp, tp, vp]
+            lib.gmm_widen_mxfp4_run.argtypes = [vp, vp, vp, vp, vp]
             lib.gmm_widen_mxfp4_run.restype = ctypes.c_int
             _lib = lib
     return _lib

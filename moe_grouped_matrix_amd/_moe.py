@@ -7,50 +7,97 @@ are the library's."""
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional
 
 import torch
 
-from ._binding import (_DTYPE, _raise, _ref, _view, _view_packed, GMM_E_INVALID, GMM_I64, GmmInvalid, handle, load)
+from ._binding import (_DTYPE, _handles, _raise, GMM_E_INVALID, GMM_F4E2M1, GMM_I64, GmmInvalid, GmmTensor, handle,
+                       load)
 
 EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatch_run", "gmm_combine_run",
                 "gmm_combine_grad_run", "gmm_quant_mxfp4_run", "gmm_widen_mxfp4_run")
 FLAG_BAD_ROW = 0x10
 
 _ID_DTYPE = {torch.int32: _DTYPE[torch.int32], torch.int64: GMM_I64}
+_PACKED_DTYPE = {torch.uint8: GMM_F4E2M1, torch.float4_e2m1fn_x2: GMM_F4E2M1}
+
+# These calls take a few microseconds on the GPU for a decode step, so the
+# host's share counts: a gmm_tensor is packed as the bytes of the C struct
+# (0.5 us against 1.5 us for a ctypes structure), and the current stream is
+# taken as the raw handle (0.2 us against 3 us for a Stream object).
+_TENSOR = struct.Struct("@Piiqqqq")
+assert _TENSOR.size == ctypes.sizeof(GmmTensor)
+_PAD = [(0,) * (4 - n) for n in range(5)]
 
 
-class _Call:
-    """The views, stream and handle of one call.  Every tensor lives on the
-    first one's device; outputs that the call makes are allocated on the stream
-    that writes them, and kept from reuse while the current stream may still
-    read them."""
+def _refuse(text: str):
+    raise GmmInvalid(GMM_E_INVALID, text)
 
-    def __init__(self, stream: Optional[torch.cuda.Stream], first: torch.Tensor, name: str):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise GmmInvalid(GMM_E_INVALID, f"{name} must be a device tensor")
-        self.dev = first.device
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.dev)
-        if self.stream.device != self.dev:
-            raise GmmInvalid(GMM_E_INVALID, f"the stream is on {self.stream.device}, {name} on {self.dev}")
 
-    def view(self, t: Optional[torch.Tensor], name: str, packed: bool = False, dtypes=_DTYPE):
-        if t is not None and t.is_cuda and t.device != self.dev:
-            raise GmmInvalid(GMM_E_INVALID, f"{name} is on {t.device}, not on {self.dev}")
-        return _view_packed(t, "fp4_e2m1", name) if packed else _view(t, name, dtypes)
+def _pack(t: torch.Tensor, name: str, dev: torch.device, dtypes=_DTYPE) -> bytes:
+    """The C struct of a dense tensor on `dev`.  Packed four-bit bytes
+    (dtypes _PACKED_DTYPE) count elements, two to a byte of the last
+    dimension."""
+    if not t.is_cuda:
+        _refuse(f"{name} must be a device tensor")
+    if t.device != dev:
+        _refuse(f"{name} is on {t.device}, not on {dev}")
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    code = dtypes.get(t.dtype)
+    if code is None:
+        _refuse(f"{name}: unsupported dtype {t.dtype}")
+    shape = t.shape
+    n = len(shape)
+    if n > 4 or (n == 0 and dtypes is _PACKED_DTYPE):
+        _refuse(f"{name}: rank {n} is not supported")
+    if dtypes is _PACKED_DTYPE:
+        shape = (*shape[:-1], 2 * shape[-1])
+    return _TENSOR.pack(t.data_ptr() if t.numel() else 0, code, n, *shape, *_PAD[n])
 
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        current = torch.cuda.current_stream(self.dev)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if current != self.stream:
-            t.record_stream(current)
-        return t
 
-    def run(self, name: str, *args) -> None:
-        h = handle(self.dev)
-        _raise(getattr(load(), name)(h, *[_ref(a) if hasattr(a, "_fields_") else a for a in args],
-                                     ctypes.c_void_p(self.stream.cuda_stream)), h)
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    load()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(f"{name} must be a device tensor")
+    return t.device
+
+
+def _empty(shape, dtype: torch.dtype, dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """An output or workspace for a call on `stream` (None: the current one):
+    allocated on the stream that writes it, and kept from reuse while the
+    current stream may still read it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    current = torch.cuda.current_stream(dev)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
+def _run(name: str, dev: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        _refuse(f"the stream is on {stream.device}, the tensors on {dev}")
+    else:
+        raw = stream.cuda_stream
+    h = _handles.get(dev.index) or handle(dev)
+    status = getattr(load(), name)(h, *args, raw)
+    if status:
+        _raise(status, h)
+
+
+@functools.lru_cache(maxsize=4096)
+def _sort_workspace(slots: int, groups: int) -> int:
+    need = ctypes.c_size_t(0)
+    # a refused size is the run's to report, with its text
+    load().gmm_sort_tokens_workspace(slots, groups, ctypes.byref(need))
+    return need.value
 
 
 def sort_tokens(expert_ids: torch.Tensor, num_groups: int, *,
@@ -64,21 +111,19 @@ def sort_tokens(expert_ids: torch.Tensor, num_groups: int, *,
     [T,k], each slot's row in the sorted order).  An id outside [0, num_groups)
     leaves its slot unrouted: its row comes after all others, and slot_row
     holds the row's bitwise complement (a negative number)."""
-    load()
-    c = _Call(stream, expert_ids, "expert_ids")
-    ids = c.view(expert_ids, "expert_ids", dtypes=_ID_DTYPE)
-    need = ctypes.c_size_t(0)
-    # a refused size is the run's to report, with its text
-    load().gmm_sort_tokens_workspace(expert_ids.numel(), int(num_groups), ctypes.byref(need))
+    dev = _device(expert_ids, "expert_ids")
+    ids = _pack(expert_ids, "expert_ids", dev, _ID_DTYPE)
+    groups = int(num_groups)
     if group_sizes is None:
-        group_sizes = c.empty((max(int(num_groups), 0),), torch.int32)
-    elif group_sizes.dim() != 1 or group_sizes.numel() != int(num_groups):
-        raise GmmInvalid(GMM_E_INVALID, "group_sizes must hold num_groups elements")
+        group_sizes = _empty((max(groups, 0),), torch.int32, dev, stream)
+    elif group_sizes.dim() != 1 or group_sizes.numel() != groups:
+        _refuse("group_sizes must hold num_groups elements")
     if slot_row is None:
-        slot_row = c.empty(tuple(expert_ids.shape), torch.int32)
-    work = c.empty((need.value,), torch.uint8) if need.value else None
-    c.run("gmm_sort_tokens_run", ids, c.view(group_sizes, "group_sizes"), c.view(slot_row, "slot_row"),
-          ctypes.c_void_p(work.data_ptr() if work is not None else None), need)
+        slot_row = _empty(expert_ids.shape, torch.int32, dev, stream)
+    need = _sort_workspace(expert_ids.numel(), groups)
+    work = _empty((need,), torch.uint8, dev, stream) if need else None
+    _run("gmm_sort_tokens_run", dev, stream, ids, _pack(group_sizes, "group_sizes", dev),
+         _pack(slot_row, "slot_row", dev), work.data_ptr() if need else None, need)
     return group_sizes, slot_row
 
 
@@ -88,12 +133,11 @@ def dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, out: Optional[torch.Ten
     rows[slot_row[t,j]] = x[t], the rows of unrouted slots zeros.  x [T,D] of
     any one-, two- or four-byte dtype, slot_row from sort_tokens(); returns
     rows [T*k,D], the lhs of gmm().  The gradient is combine(drows, slot_row)."""
-    load()
-    c = _Call(stream, x, "x")
-    views = [c.view(x, "x"), c.view(slot_row, "slot_row")]
+    dev = _device(x, "x")
+    xv, sv = _pack(x, "x", dev), _pack(slot_row, "slot_row", dev)
     if out is None:
-        out = c.empty((slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype)
-    c.run("gmm_dispatch_run", *views, c.view(out, "out"))
+        out = _empty((slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype, dev, stream)
+    _run("gmm_dispatch_run", dev, stream, xv, sv, _pack(out, "out", dev))
     return out
 
 
@@ -105,13 +149,13 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.
     float32, rounded once.  rows [T*k,D] and weights [T,k] float32 or bfloat16
     (weights None: all 1, the gradient of dispatch()); returns out [T,D] of
     out_dtype (rows' dtype by default)."""
-    load()
-    c = _Call(stream, rows, "rows")
-    views = [c.view(rows, "rows"), c.view(slot_row, "slot_row"), c.view(weights, "weights")]
+    dev = _device(rows, "rows")
+    rv, sv = _pack(rows, "rows", dev), _pack(slot_row, "slot_row", dev)
+    wv = _pack(weights, "weights", dev) if weights is not None else None
     if out is None:
-        out = c.empty((slot_row.shape[0] if slot_row.dim() else 0, rows.shape[1] if rows.dim() == 2 else 0),
-                      out_dtype if out_dtype is not None else rows.dtype)
-    c.run("gmm_combine_run", *views, c.view(out, "out"))
+        out = _empty((slot_row.shape[0] if slot_row.dim() else 0, rows.shape[1] if rows.dim() == 2 else 0),
+                     out_dtype if out_dtype is not None else rows.dtype, dev, stream)
+    _run("gmm_combine_run", dev, stream, rv, sv, wv, _pack(out, "out", dev))
     return out
 
 
@@ -121,24 +165,24 @@ def combine_grad(dout: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
     """The gradients of combine() with weights, through libgmm.so
     (gmm_combine_grad_run).  Returns (drows [T*k,D] of rows' dtype, zeros in
     the rows of unrouted slots; dweights [T,k] of weights' dtype, 0 there)."""
-    load()
-    c = _Call(stream, dout, "dout")
-    views = [c.view(dout, "dout"), c.view(rows, "rows"), c.view(slot_row, "slot_row"), c.view(weights, "weights")]
+    dev = _device(dout, "dout")
     if weights is None:
-        raise GmmInvalid(GMM_E_INVALID, "weights are required (without them the gradient is dispatch())")
+        _refuse("weights are required (without them the gradient is dispatch())")
+    views = [_pack(t, n, dev) for t, n in ((dout, "dout"), (rows, "rows"), (slot_row, "slot_row"),
+                                           (weights, "weights"))]
     if drows is None:
-        drows = c.empty(tuple(rows.shape), rows.dtype)
+        drows = _empty(rows.shape, rows.dtype, dev, stream)
     if dweights is None:
-        dweights = c.empty(tuple(weights.shape), weights.dtype)
-    c.run("gmm_combine_grad_run", *views, c.view(drows, "drows"), c.view(dweights, "dweights"))
+        dweights = _empty(weights.shape, weights.dtype, dev, stream)
+    _run("gmm_combine_grad_run", dev, stream, *views, _pack(drows, "drows", dev), _pack(dweights, "dweights", dev))
     return drows, dweights
 
 
 def _operand(operand: str, dims: int, name: str) -> None:
     if operand not in ("lhs", "rhs"):
-        raise GmmInvalid(GMM_E_INVALID, f"operand must be 'lhs' or 'rhs', got {operand!r}")
+        _refuse(f"operand must be 'lhs' or 'rhs', got {operand!r}")
     if dims != (2 if operand == "lhs" else 3):
-        raise GmmInvalid(GMM_E_INVALID, f"{name}: a {operand} is a {2 if operand == 'lhs' else 3}-tensor")
+        _refuse(f"{name}: a {operand} is a {2 if operand == 'lhs' else 3}-tensor")
 
 
 def quant_mxfp4(x: torch.Tensor, *, operand: str = "lhs", q: Optional[torch.Tensor] = None,
@@ -149,17 +193,17 @@ def quant_mxfp4(x: torch.Tensor, *, operand: str = "lhs", q: Optional[torch.Tens
     layouts that gmm() takes: operand "lhs" x [M,K] -> scale [M,K/32] (with
     lhs_format="fp4_e2m1"), "rhs" x [Ga,N,K] -> scale [Ga,K/32,1,N] (with
     rhs_format="fp4_e2m1")."""
-    load()
-    c = _Call(stream, x, "x")
+    dev = _device(x, "x")
     _operand(operand, x.dim(), "x")
-    xv = c.view(x, "x")
-    K = x.shape[-1]
+    xv = _pack(x, "x", dev)
+    shape = x.shape
+    K = shape[-1]
     if q is None:
-        q = c.empty(tuple(x.shape[:-1]) + (K // 2,), torch.uint8)
+        q = _empty((*shape[:-1], K // 2), torch.uint8, dev, stream)
     if scale is None:
-        scale = c.empty((x.shape[0], K // 32) if operand == "lhs" else (x.shape[0], K // 32, 1, x.shape[1]),
-                        torch.float8_e8m0fnu)
-    c.run("gmm_quant_mxfp4_run", xv, c.view(q, "q", packed=True), c.view(scale, "scale"))
+        scale = _empty((shape[0], K // 32) if operand == "lhs" else (shape[0], K // 32, 1, shape[1]),
+                       torch.float8_e8m0fnu, dev, stream)
+    _run("gmm_quant_mxfp4_run", dev, stream, xv, _pack(q, "q", dev, _PACKED_DTYPE), _pack(scale, "scale", dev))
     return q, scale
 
 
@@ -169,11 +213,10 @@ def widen_mxfp4(q: torch.Tensor, scale: torch.Tensor, *, operand: str = "lhs",
     """The values of a microscaled fp4 tensor through libgmm.so
     (gmm_widen_mxfp4_run), exact in bfloat16 and float32: q and scale as
     quant_mxfp4() returns them for the same operand; returns [...,K]."""
-    load()
-    c = _Call(stream, q, "q")
+    dev = _device(q, "q")
     _operand(operand, q.dim(), "q")
-    views = [c.view(q, "q", packed=True), c.view(scale, "scale")]
+    qv, sv = _pack(q, "q", dev, _PACKED_DTYPE), _pack(scale, "scale", dev)
     if out is None:
-        out = c.empty(tuple(q.shape[:-1]) + (2 * q.shape[-1],), out_dtype)
-    c.run("gmm_widen_mxfp4_run", *views, c.view(out, "out"))
+        out = _empty((*q.shape[:-1], 2 * q.shape[-1]), out_dtype, dev, stream)
+    _run("gmm_widen_mxfp4_run", dev, stream, qv, sv, _pack(out, "out", dev))
     return out

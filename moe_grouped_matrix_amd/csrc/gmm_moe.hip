@@ -17,11 +17,36 @@ namespace {
 // Stable sort by expert.  A counting sort: row(s) = (slots of smaller keys) +
 // (earlier slots of the same key), the key of an unrouted slot being G.  The
 // slots are cut into contiguous runs, one per workgroup; the first launch
-// counts every run's keys, and in the second each workgroup adds up the counts
-// of all runs (what stands before its own, and the totals) and ranks its
-// slots.  Within a wave equal keys find each other by one ballot per key bit;
+// counts every run's keys (kept key by key, so that a wave reads a key's counts
+// with one load a lane), and in the second each workgroup adds up the counts of
+// all runs (what stands before its own, and the totals) and ranks its slots.  Within a wave equal keys find each other by one ballot per key bit;
 // a wave takes 64 consecutive slots at a time, in order, so the rank of a slot
 // is its wave's running count plus the equal lanes below it.
+
+// Sum over the wave's lanes, by row shifts and row broadcasts (every lane gets
+// it; the order of the additions is fixed).
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0x111, 0xF>(v);
+  v += dpp_f32<0x112, 0xF>(v);
+  v += dpp_f32<0x114, 0xF>(v);
+  v += dpp_f32<0x118, 0xF>(v);
+  v += dpp_f32<0x142, 0xA>(v);
+  v += dpp_f32<0x143, 0xC>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 
 __device__ __forceinline__ int sort_key(const SortParams& p, long long i) {
   const long long id = p.ids64 ? reinterpret_cast<const int64_t*>(p.ids)[i]
@@ -36,8 +61,7 @@ __global__ __launch_bounds__(kSortCountT) void sort_count_kernel(SortParams p) {
   const long long lo = blockIdx.x * p.per, hi = lo + p.per < p.n ? lo + p.per : p.n;
   for (long long i = lo + threadIdx.x; i < hi; i += kSortCountT) atomicAdd(&hist[sort_key(p, i)], 1);
   __syncthreads();
-  int32_t* const ws = p.counts + (long long)blockIdx.x * (p.G + 1);
-  for (int g = threadIdx.x; g <= p.G; g += kSortCountT) ws[g] = hist[g];
+  for (int g = threadIdx.x; g <= p.G; g += kSortCountT) p.counts[(long long)g * gridDim.x + blockIdx.x] = hist[g];
 }
 
 template <int T>
@@ -55,15 +79,25 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
   const int bits = 32 - __builtin_clz(p.G);  // keys 0 .. G
   const long long lo = blockIdx.x * p.per, hi = lo + p.per < p.n ? lo + p.per : p.n;
 
-  for (int g = tid; g < S; g += T) base[g] = total[g] = 0;
-  __syncthreads();
-  if (!alone) {
-    for (int b = w; b < (int)gridDim.x; b += W) {
-      const int32_t* const ws = p.counts + (long long)b * S;
-      for (int g = lane; g < S; g += 64) {
-        const int c = ws[g];
-        atomicAdd(&total[g], c);
-        if (b < (int)blockIdx.x) atomicAdd(&base[g], c);
+  if (alone) {
+    for (int g = tid; g < S; g += T) base[g] = 0;
+  } else {
+    const int B = gridDim.x;  // at most kSortBlocks
+    for (int g = w; g < S; g += W) {
+      const int32_t* const ws = p.counts + (long long)g * B;
+      int all = 0, before = 0;
+#pragma unroll
+      for (int i = 0; i < kSortBlocks / 64; ++i) {
+        const int b = lane + 64 * i;
+        const int c = b < B ? ws[b] : 0;
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
+      }
+      all = wave_sum(all);
+      before = wave_sum(before);
+      if (lane == 0) {
+        total[g] = all;
+        base[g] = before;
       }
     }
   }
@@ -152,19 +186,49 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows.  A wave takes one token's columns in chunks of V elements per lane.  A
-// row whose width is not a multiple of V ends in a chunk that starts V before
-// the end and overlaps the chunk before it (both write the same values); rows
-// narrower than V go one element at a time.
+// Rows.  All three kernels stream rows once and are HBM-bound; what they need
+// is many independent 16-byte loads in flight.  A wave takes one token and up
+// to U chunks of V elements a lane (a segment of its columns), and loads the
+// token's slot entries (k <= 64) with one load, a slot a lane; the slots' rows
+// then come from lanes into scalar registers, so that a row's address is a
+// scalar and its rows' loads do not wait for one another.  A row whose width
+// is not a multiple of V ends in a chunk that starts V before its end and
+// overlaps the one before (both write the same values); rows narrower than V
+// go one element at a time.  Rows start at any multiple of the element size.
+
+typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 template <typename E, int V>
 struct Vec {
   E v[V];
 };
 
-template <int V>
-__device__ __forceinline__ int chunk_start(int c, int D) {
-  return c * V + V <= D ? c * V : D - V;
+template <typename E, int V>
+__device__ __forceinline__ Vec<E, V> load_vec(const E* p) {
+  Vec<E, V> r;
+  constexpr int B = sizeof(E) * V;
+  if constexpr (B % 16 == 0) {
+    i32x4 w[B / 16];
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4_any*>(p) + i);
+    __builtin_memcpy(&r, w, B);
+  } else {
+    __builtin_memcpy(&r, p, B);
+  }
+  return r;
+}
+template <typename E, int V>
+__device__ __forceinline__ void store_vec(E* p, const Vec<E, V>& r) {
+  constexpr int B = sizeof(E) * V;
+  if constexpr (B % 16 == 0) {
+    i32x4 w[B / 16];
+    __builtin_memcpy(w, &r, B);
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i)
+      __builtin_nontemporal_store((i32x4_any)w[i], reinterpret_cast<i32x4_any*>(p) + i);
+  } else {
+    __builtin_memcpy(p, &r, B);
+  }
 }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -172,137 +236,227 @@ __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v)
 __device__ __forceinline__ void from_f32(float f, float& v) { v = f; }
 __device__ __forceinline__ void from_f32(float f, uint16_t& v) { v = f32_to_bf16_rne(f); }
 
-// rows start at any multiple of the element size: the copies say so
-template <typename E, int V>
-__device__ __forceinline__ Vec<E, V> load_vec(const E* p) {
-  Vec<E, V> r;
-  __builtin_memcpy(&r, p, sizeof r);
-  return r;
-}
-template <typename E, int V>
-__device__ __forceinline__ void store_vec(E* p, const Vec<E, V>& r) {
-  __builtin_memcpy(p, &r, sizeof r);
+// The slot entries of token t, slot j in lane j: the row it names (as itself
+// or as a complement), -1 for none or for one outside [0, n) (flagged), and
+// whether the slot is routed.
+struct Slots {
+  int row, routed;
+  float w;
+};
+
+__device__ __forceinline__ Slots load_slots(const RowParams& p, long long t, int lane) {
+  Slots s{-1, 0, 0.f};
+  if (lane < p.k) {
+    const long long i = t * p.k + lane;
+    const int r = p.slot_row[i];
+    s.row = r < 0 ? ~r : r;
+    s.routed = r >= 0;
+    if (s.row >= p.n) {
+      s.row = -1;
+      atomicOr(p.flags, kFlagBadRow);
+    }
+    s.w = 1.f;
+    if (p.weights)
+      s.w = p.w_f32 ? static_cast<const float*>(p.weights)[i]
+                    : bf16_bits_to_f32(static_cast<const uint16_t*>(p.weights)[i]);
+  }
+  return s;
 }
 
-__device__ __forceinline__ void bad_row(const RowParams& p) { atomicOr(p.flags, kFlagBadRow); }
-
-// The row that slot entry r names (as itself or as a complement), or -1 and
-// the flag for one outside [0, n).
-__device__ __forceinline__ int named_row(const RowParams& p, int r, int lane) {
-  const int row = r < 0 ? ~r : r;
-  if (row < p.n) return row;
-  if (lane == 0) bad_row(p);
-  return -1;
+__device__ __forceinline__ int of_lane(int v, int j) { return __builtin_amdgcn_readlane(v, j); }
+__device__ __forceinline__ float of_lane(float v, int j) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
 }
 
+// First element of the chunk that chunk number c of a row covers.
 template <int V>
+__device__ __forceinline__ int chunk_start(int c, int D) {
+  return c * V + V <= D ? c * V : D - V;
+}
+
+// Work item i of a row kernel: a token and a segment of 64 U chunks.
+struct RowItem {
+  long long t;
+  int c0, chunks;
+};
+
+template <int V, int U>
+__device__ __forceinline__ RowItem row_item(const RowParams& p, long long i) {
+  const int chunks = (p.D + V - 1) / V, segs = (chunks + 64 * U - 1) / (64 * U);
+  if (segs == 1) return {p.t0 + i, 0, chunks};
+  const long long t = i / segs;
+  return {p.t0 + t, (int)(i - t * segs) * 64 * U, chunks};
+}
+
+template <int V, int U>
 __global__ __launch_bounds__(kRowT) void dispatch_kernel(RowParams p) {
   const int lane = threadIdx.x & 63;
+  const long long item = (long long)blockIdx.x * (kRowT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowItem it = row_item<V, U>(p, item);
+  if (it.t >= p.t1) return;
   const int D = p.D;  // bytes of a row
-  const int chunks = (D + V - 1) / V;
-  const long long waves = (long long)gridDim.x * (kRowT / 64);
-  for (long long t = (long long)blockIdx.x * (kRowT / 64) + (threadIdx.x >> 6); t < p.T; t += waves) {
-    const uint8_t* const src = static_cast<const uint8_t*>(p.a) + t * D;
-    for (int c = lane; c < chunks; c += 64) {
-      const int at = chunk_start<V>(c, D);
-      const Vec<uint8_t, V> x = load_vec<uint8_t, V>(src + at);
-      for (int j = 0; j < p.k; ++j) {
-        const int r = p.slot_row[t * p.k + j];
-        const int row = named_row(p, r, lane);
-        if (row < 0) continue;
-        Vec<uint8_t, V> v = x;
-        if (r < 0) v = Vec<uint8_t, V>{};
-        store_vec(static_cast<uint8_t*>(p.out) + (long long)row * D + at, v);
-      }
+  const uint8_t* const src = static_cast<const uint8_t*>(p.a) + it.t * D;
+  int at[U];
+  Vec<uint8_t, V> x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = it.c0 + 64 * u + lane;
+    at[u] = c < it.chunks ? chunk_start<V>(c, D) : -1;
+    if (at[u] >= 0) x[u] = load_vec<uint8_t, V>(src + at[u]);
+  }
+  const Slots s = load_slots(p, it.t, lane);
+  for (int j = 0; j < p.k; ++j) {
+    const int row = of_lane(s.row, j);
+    if (row < 0) continue;
+    uint8_t* const dst = static_cast<uint8_t*>(p.out) + (long long)row * D;
+    if (of_lane(s.routed, j)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at[u] >= 0) store_vec(dst + at[u], x[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at[u] >= 0) store_vec(dst + at[u], Vec<uint8_t, V>{});
     }
   }
 }
 
-// out[t] = sum over j of w[t,j] * rows[slot_row[t,j]]
-template <typename R, typename O, int V>
+// out[t] = sum over j of w[t,j] * rows[slot_row[t,j]], four rows in flight
+template <typename R, typename O, int V, int U>
 __global__ __launch_bounds__(kRowT) void combine_kernel(RowParams p) {
+  constexpr int JB = 4;
   const int lane = threadIdx.x & 63;
+  const long long item = (long long)blockIdx.x * (kRowT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowItem it = row_item<V, U>(p, item);
+  if (it.t >= p.t1) return;
   const int D = p.D;
-  const int chunks = (D + V - 1) / V;
-  const long long waves = (long long)gridDim.x * (kRowT / 64);
-  for (long long t = (long long)blockIdx.x * (kRowT / 64) + (threadIdx.x >> 6); t < p.T; t += waves) {
-    for (int c = lane; c < chunks; c += 64) {
-      const int at = chunk_start<V>(c, D);
-      float acc[V];
+  const Slots s = load_slots(p, it.t, lane);
+  int at[U];
+  float acc[U][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.f;
-      for (int j = 0; j < p.k; ++j) {
-        const int r = p.slot_row[t * p.k + j];
-        const int row = named_row(p, r, lane);
-        if (r < 0 || row < 0) continue;
-        float w = 1.f;
-        if (p.weights) w = p.w_f32 ? static_cast<const float*>(p.weights)[t * p.k + j]
-                                   : bf16_bits_to_f32(static_cast<const uint16_t*>(p.weights)[t * p.k + j]);
-        const Vec<R, V> x = load_vec<R, V>(static_cast<const R*>(p.a) + (long long)row * D + at);
+  for (int u = 0; u < U; ++u) {
+    const int c = it.c0 + 64 * u + lane;
+    at[u] = c < it.chunks ? chunk_start<V>(c, D) : -1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, to_f32(x.v[i]), acc[i]);
-      }
-      Vec<O, V> o;
+    for (int e = 0; e < V; ++e) acc[u][e] = 0.f;
+  }
+  for (int j = 0; j < p.k; j += JB) {
+    Vec<R, V> x[JB][U];
+    bool live[JB];
 #pragma unroll
-      for (int i = 0; i < V; ++i) from_f32(acc[i], o.v[i]);
-      store_vec(static_cast<O*>(p.out) + t * D + at, o);
+    for (int b = 0; b < JB; ++b) {
+      // (lanes past k hold no row)
+      const int row = j + b < p.k ? of_lane(s.row, j + b) : -1;
+      live[b] = row >= 0 && of_lane(s.routed, j + b < p.k ? j + b : 0);
+      if (!live[b]) continue;
+      const R* const src = static_cast<const R*>(p.a) + (long long)row * D;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at[u] >= 0) x[b][u] = load_vec<R, V>(src + at[u]);
     }
+#pragma unroll
+    for (int b = 0; b < JB; ++b) {
+      if (!live[b]) continue;
+      const float w = of_lane(s.w, j + b);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[u][e] = __builtin_fmaf(w, to_f32(x[b][u].v[e]), acc[u][e]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (at[u] < 0) continue;
+    Vec<O, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) from_f32(acc[u][e], o.v[e]);
+    store_vec(static_cast<O*>(p.out) + it.t * D + at[u], o);
   }
 }
 
-// drows[slot_row[t,j]] = w[t,j] * dout[t], dweights[t,j] = <dout[t], rows[slot_row[t,j]]>
-template <typename G, typename R, int V>
+// drows[slot_row[t,j]] = w[t,j] * dout[t], dweights[t,j] = <dout[t], rows[slot_row[t,j]]>.
+// A wave takes p.part of a token's slots over all its columns, so a product's
+// sum never leaves the wave: per segment it is added up over the lanes, and
+// lane j keeps slot j's.
+template <typename G, typename R, int V, int U>
 __global__ __launch_bounds__(kRowT) void combine_grad_kernel(RowParams p) {
+  constexpr int JB = 2;
   const int lane = threadIdx.x & 63;
-  const int D = p.D;
-  const int chunks = (D + V - 1) / V;
-  const long long waves = (long long)gridDim.x * (kRowT / 64);
-  const long long slots = p.T * p.k;
-  for (long long s = (long long)blockIdx.x * (kRowT / 64) + (threadIdx.x >> 6); s < slots; s += waves) {
-    const long long t = s / p.k;
-    const int r = p.slot_row[s];
-    const int row = named_row(p, r, lane);
-    float dot = 0.f;
-    if (row >= 0) {
-      const float w = r < 0 ? 0.f
-                            : (p.w_f32 ? static_cast<const float*>(p.weights)[s]
-                                       : bf16_bits_to_f32(static_cast<const uint16_t*>(p.weights)[s]));
-      const G* const g = static_cast<const G*>(p.b) + t * D;
-      const R* const x = static_cast<const R*>(p.a) + (long long)row * D;
-      R* const o = static_cast<R*>(p.out) + (long long)row * D;
-      for (int c = lane; c < chunks; c += 64) {
-        const int at = chunk_start<V>(c, D);
-        Vec<R, V> d{};
-        if (r >= 0) {
-          const Vec<G, V> gv = load_vec<G, V>(g + at);
-          const Vec<R, V> xv = load_vec<R, V>(x + at);
+  const long long item = (long long)blockIdx.x * (kRowT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int parts = (p.k + p.part - 1) / p.part;
+  const long long rel = parts == 1 ? item : item / parts, t = p.t0 + rel;
+  if (t >= p.t1) return;
+  const int j0 = parts == 1 ? 0 : (int)(item - rel * parts) * p.part;
+  const int j1 = j0 + p.part < p.k ? j0 + p.part : p.k;
+  const int D = p.D, chunks = (D + V - 1) / V;
+  const Slots s = load_slots(p, t, lane);
+  const G* const g = static_cast<const G*>(p.b) + t * D;
+  float mine = 0.f;
+  for (int c0 = 0; c0 < chunks; c0 += 64 * U) {
+    int at[U];
+    Vec<G, V> gv[U];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float gi = to_f32(gv.v[i]);
-            // elements of an overlapping last chunk count once
-            if (at + i >= c * V) dot = __builtin_fmaf(gi, to_f32(xv.v[i]), dot);
-            from_f32(w * gi, d.v[i]);
-          }
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + 64 * u + lane;
+      at[u] = c < chunks ? chunk_start<V>(c, D) : -1;
+      gv[u] = Vec<G, V>{};
+      if (at[u] >= 0) gv[u] = load_vec<G, V>(g + at[u]);
+    }
+    // elements of the last chunk that the one before has: they count once
+    const bool tail = c0 + 64 * U >= chunks && D % V != 0;
+    for (int j = j0; j < j1; j += JB) {
+      Vec<R, V> x[JB][U];
+      int row[JB];
+      bool routed[JB];
+#pragma unroll
+      for (int b = 0; b < JB; ++b) {
+        const int jb = j + b < j1 ? j + b : j;
+        row[b] = j + b < j1 ? of_lane(s.row, jb) : -1;
+        routed[b] = row[b] >= 0 && of_lane(s.routed, jb);
+        if (!routed[b]) continue;
+        const R* const src = static_cast<const R*>(p.a) + (long long)row[b] * D;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[b][u] = Vec<R, V>{};
+          if (at[u] >= 0) x[b][u] = load_vec<R, V>(src + at[u]);
         }
-        store_vec(o + at, d);
+      }
+#pragma unroll
+      for (int b = 0; b < JB; ++b) {
+        if (row[b] < 0) continue;
+        R* const dst = static_cast<R*>(p.out) + (long long)row[b] * D;
+        if (!routed[b]) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (at[u] >= 0) store_vec(dst + at[u], Vec<R, V>{});
+          continue;
+        }
+        const float w = of_lane(s.w, j + b);
+        float dot = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<R, V> d;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float ge = to_f32(gv[u].v[e]);
+            from_f32(w * ge, d.v[e]);
+            const bool count = !tail || at[u] + e >= (c0 + 64 * u + lane) * V;
+            dot = __builtin_fmaf(count ? ge : 0.f, to_f32(x[b][u].v[e]), dot);
+          }
+          if (at[u] >= 0) store_vec(dst + at[u], d);
+        }
+        dot = wave_sum(dot);
+        if (lane == j + b) mine += dot;
       }
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
-    if (lane == 0) {
-      if (p.w_f32)
-        static_cast<float*>(p.dweights)[s] = dot;
-      else
-        static_cast<uint16_t*>(p.dweights)[s] = f32_to_bf16_rne(dot);
-    }
   }
-}
-
-unsigned row_grid(long long items, int cu_count) {
-  long long grid = (items + kRowT / 64 - 1) / (kRowT / 64);
-  const long long cap = (long long)cu_count * 32;
-  if (grid > cap) grid = cap;
-  return (unsigned)(grid < 1 ? 1 : grid);
+  if (lane >= j0 && lane < j1) {
+    const long long i = t * p.k + lane;
+    if (p.w_f32)
+      static_cast<float*>(p.dweights)[i] = mine;
+    else
+      static_cast<uint16_t*>(p.dweights)[i] = f32_to_bf16_rne(mine);
+  }
 }
 
 }  // namespace
@@ -313,54 +467,103 @@ hipError_t launch_sort(const SortParams& p, int blocks, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (p.per <= 1024)
+  if (blocks > 1)
+    hipLaunchKernelGGL(sort_place_kernel<512>, dim3((unsigned)blocks), dim3(512), 0, stream, p);
+  else if (p.per <= 1024)
     hipLaunchKernelGGL(sort_place_kernel<256>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
   else
     hipLaunchKernelGGL(sort_place_kernel<1024>, dim3((unsigned)blocks), dim3(1024), 0, stream, p);
   return hipGetLastError();
 }
 
+// Chunks a lane takes: a whole row in one segment up to four a lane, but with
+// too few tokens to fill the card one, so that more waves share the rows.
+static int row_unroll(long long tokens, int D, int V, int cu) {
+  const int chunks = (D + V - 1) / V;
+  const int u = (chunks + 63) / 64;
+  if (tokens < 8LL * cu) return 1;
+  return u > 4 ? 4 : u;
+}
+
+// Runs launch(p, blocks) over all tokens with `per_token` waves each, in
+// slices of tokens that keep a launch below 2^31 threads.
+template <class LaunchFn>
+static hipError_t by_slices(RowParams p, long long per_token, LaunchFn launch) {
+  const long long most = (1LL << 25) / per_token > 0 ? (1LL << 25) / per_token : 1;
+  for (p.t0 = 0; p.t0 < p.T; p.t0 = p.t1) {
+    p.t1 = p.t0 + most < p.T ? p.t0 + most : p.T;
+    launch(p, (unsigned)(((p.t1 - p.t0) * per_token + kRowT / 64 - 1) / (kRowT / 64)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+static long long row_segs(const RowParams& p, int V, int U) { return ((p.D + V - 1LL) / V + 64 * U - 1) / (64 * U); }
+
+#define GMM_LAUNCH(KERNEL) hipLaunchKernelGGL(KERNEL, dim3(blocks), dim3(kRowT), 0, st, q)
+
+template <int V, int U>
+static hipError_t dispatch_u(const RowParams& p, hipStream_t st) {
+  return by_slices(p, row_segs(p, V, U),
+                   [=](const RowParams& q, unsigned blocks) { GMM_LAUNCH((dispatch_kernel<V, U>)); });
+}
+
 hipError_t launch_dispatch(const RowParams& p, int cu, hipStream_t st) {
-  const unsigned grid = row_grid(p.T, cu);
-  if (p.D >= 16)
-    hipLaunchKernelGGL(dispatch_kernel<16>, dim3(grid), dim3(kRowT), 0, st, p);
-  else
-    hipLaunchKernelGGL(dispatch_kernel<1>, dim3(grid), dim3(kRowT), 0, st, p);
-  return hipGetLastError();
+  if (p.D < 16) return dispatch_u<1, 1>(p, st);
+  switch (row_unroll(p.T, p.D, 16, cu)) {
+    case 1: return dispatch_u<16, 1>(p, st);
+    case 2: return dispatch_u<16, 2>(p, st);
+    case 3: return dispatch_u<16, 3>(p, st);
+    default: return dispatch_u<16, 4>(p, st);
+  }
+}
+
+template <typename R, typename O, int V, int U>
+static hipError_t combine_u(const RowParams& p, hipStream_t st) {
+  return by_slices(p, row_segs(p, V, U),
+                   [=](const RowParams& q, unsigned blocks) { GMM_LAUNCH((combine_kernel<R, O, V, U>)); });
 }
 
 template <typename R, typename O>
-static void combine_by_width(const RowParams& p, unsigned grid, hipStream_t st) {
-  if (p.D >= 8)
-    hipLaunchKernelGGL((combine_kernel<R, O, 8>), dim3(grid), dim3(kRowT), 0, st, p);
-  else
-    hipLaunchKernelGGL((combine_kernel<R, O, 1>), dim3(grid), dim3(kRowT), 0, st, p);
+static hipError_t combine_by_width(const RowParams& p, int cu, hipStream_t st) {
+  if (p.D < 8) return combine_u<R, O, 1, 1>(p, st);
+  switch (row_unroll(p.T, p.D, 8, cu)) {
+    case 1: return combine_u<R, O, 8, 1>(p, st);
+    case 2: return combine_u<R, O, 8, 2>(p, st);
+    case 3: return combine_u<R, O, 8, 3>(p, st);
+    default: return combine_u<R, O, 8, 4>(p, st);
+  }
 }
 
 hipError_t launch_combine(const RowParams& p, bool rows_f32, bool out_f32, int cu, hipStream_t st) {
-  const unsigned grid = row_grid(p.T, cu);
-  if (rows_f32)
-    out_f32 ? combine_by_width<float, float>(p, grid, st) : combine_by_width<float, uint16_t>(p, grid, st);
-  else
-    out_f32 ? combine_by_width<uint16_t, float>(p, grid, st) : combine_by_width<uint16_t, uint16_t>(p, grid, st);
-  return hipGetLastError();
+  if (rows_f32) return out_f32 ? combine_by_width<float, float>(p, cu, st) : combine_by_width<float, uint16_t>(p, cu, st);
+  return out_f32 ? combine_by_width<uint16_t, float>(p, cu, st) : combine_by_width<uint16_t, uint16_t>(p, cu, st);
+}
+
+template <typename G, typename R, int V, int U>
+static hipError_t grad_u(const RowParams& p, hipStream_t st) {
+  return by_slices(p, (p.k + p.part - 1) / p.part,
+                   [=](const RowParams& q, unsigned blocks) { GMM_LAUNCH((combine_grad_kernel<G, R, V, U>)); });
 }
 
 template <typename G, typename R>
-static void grad_by_width(const RowParams& p, unsigned grid, hipStream_t st) {
-  if (p.D >= 8)
-    hipLaunchKernelGGL((combine_grad_kernel<G, R, 8>), dim3(grid), dim3(kRowT), 0, st, p);
-  else
-    hipLaunchKernelGGL((combine_grad_kernel<G, R, 1>), dim3(grid), dim3(kRowT), 0, st, p);
+static hipError_t grad_by_width(RowParams p, int cu, hipStream_t st) {
+  // a wave takes all of a token's slots, or with too few tokens one
+  p.part = p.T < 8LL * cu ? 1 : p.k;
+  if (p.D < 8) return grad_u<G, R, 1, 1>(p, st);
+  switch (((p.D + 7) / 8 + 63) / 64) {
+    case 1: return grad_u<G, R, 8, 1>(p, st);
+    case 2: return grad_u<G, R, 8, 2>(p, st);
+    case 3: return grad_u<G, R, 8, 3>(p, st);
+    default: return grad_u<G, R, 8, 4>(p, st);
+  }
 }
+#undef GMM_LAUNCH
 
 hipError_t launch_combine_grad(const RowParams& p, bool dout_f32, bool rows_f32, int cu, hipStream_t st) {
-  const unsigned grid = row_grid(p.T * p.k, cu);
-  if (dout_f32)
-    rows_f32 ? grad_by_width<float, float>(p, grid, st) : grad_by_width<float, uint16_t>(p, grid, st);
-  else
-    rows_f32 ? grad_by_width<uint16_t, float>(p, grid, st) : grad_by_width<uint16_t, uint16_t>(p, grid, st);
-  return hipGetLastError();
+  if (dout_f32) return rows_f32 ? grad_by_width<float, float>(p, cu, st) : grad_by_width<float, uint16_t>(p, cu, st);
+  return rows_f32 ? grad_by_width<uint16_t, float>(p, cu, st) : grad_by_width<uint16_t, uint16_t>(p, cu, st);
 }
 
 }  // namespace gmmk

@@ -60,7 +60,7 @@ inline Check check_memory(std::initializer_list<const gmm_tensor*> ins, std::ini
 
 // The sort's split of the slots into contiguous runs, one per workgroup.  One
 // workgroup alone (no workspace) sorts up to kSortSmall slots.  In the split
-// sort every workgroup reads the counts of all of them, [blocks][G + 1], so
+// sort every workgroup reads the counts of all of them, [G + 1][blocks], so
 // their number falls with G.
 constexpr long long kSortSmall = 4096;
 
@@ -74,7 +74,7 @@ inline SortSplit sort_split(long long slots, long long groups) {
   long long most = 32768 / (groups + 1);
   most = most > 256 ? 256 : (most < 32 ? 32 : most);
   long long per = (slots + most - 1) / most;
-  per = (per + 1023) / 1024 * 1024;
+  per = per < 2048 ? 2048 : (per + 1023) / 1024 * 1024;
   return {(int)((slots + per - 1) / per), per};
 }
 

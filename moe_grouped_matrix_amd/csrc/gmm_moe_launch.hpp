@@ -12,6 +12,7 @@ namespace gmmk {
 constexpr uint32_t kFlagBadRow = 0x10u;
 
 constexpr int kSortCountT = 256;  // threads of the sort's counting launch
+constexpr int kSortBlocks = 256;  // most workgroups of the split sort
 constexpr int kRowT = 256;        // threads of the row kernels: four waves
 
 // Stable sort of n slots by expert: each of `blocks` workgroups takes `per`
@@ -20,7 +21,7 @@ struct SortParams {
   const void* ids;  // [n] int32 or int64
   int32_t* group_sizes;
   int32_t* slot_row;
-  int32_t* counts;  // [blocks][G + 1], with more than one workgroup
+  int32_t* counts;  // [G + 1][blocks], with more than one workgroup
   long long n, per;
   int32_t G, ids64;
 };
@@ -37,7 +38,9 @@ struct RowParams {
   void* dweights;       // gradient, of weights' type
   uint32_t* flags;
   long long T, n;
+  long long t0, t1;  // the launch's tokens
   int32_t k, D, w_f32;
+  int32_t part;  // gradient: slots of a token that one wave takes
 };
 hipError_t launch_dispatch(const RowParams& p, int cu_count, hipStream_t stream);
 hipError_t launch_combine(const RowParams& p, bool rows_f32, bool out_f32, int cu_count, hipStream_t stream);

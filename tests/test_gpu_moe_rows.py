@@ -271,3 +271,13 @@ def test_python_level_refusals():
         m.combine(x, slots)
     with pytest.raises(m.GmmInvalid):
         m.combine_grad(x, torch.zeros(8, 64, device="cuda"), slots, None)
+
+
+def test_more_tokens_than_one_launch_takes():
+    """2^26 + 77 one-byte tokens: more waves than a launch holds."""
+    import moe_grouped_matrix_amd as m
+    T = (1 << 26) + 77
+    x = torch.randint(-100, 100, (T, 1), dtype=torch.int8, device="cuda")
+    slot_row = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).view(T, 1)
+    assert torch.equal(m.dispatch(x, slot_row), x.flip(0))
+    assert m.device_flags() == 0

@@ -260,6 +260,8 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
     kc.size = gmmk::SizeClass::Small;
   else if (h->tile_policy == 2)
     kc.size = gmmk::SizeClass::Big;
+  else if (kc.mx && kc.op == gmmk::Op::BF16)
+    kc.size = gmmk::mxw_size(M, Ga);
   else
     kc.size = (M >= 8192 && M >= 512 * (Ga > 0 ? Ga : 1)) ? gmmk::SizeClass::Big : gmmk::SizeClass::Small;
 

@@ -152,20 +152,23 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
   const int M = p.M, N = p.N, K = p.K;
   const int P = gridDim.x, slot = xcd_slot(blockIdx.x, P);  // (of the fill)
   const int n_ntiles = (N + C::BN - 1) / C::BN;
-  // Every XCD gets a contiguous eighth of the tiles (they share lhs rows and,
-  // in groups of more than one tile, weights in its L2), which its workgroups
-  // take in turn.  (Whole rounds over the grid left the last round's tiles to
-  // some XCDs only: 49 against 44 us for 840 tiles on 512 workgroups.)
-  const int all_items = __builtin_amdgcn_readfirstlane(pl.n_mtiles) * n_ntiles;
+  // XCD x takes chunks x, x + 8, ... of the tiles, its workgroups in turn: as
+  // many tiles on every XCD, and a popular expert's full tiles spread over all.
+  // A chunk is a row tile with all its column tiles, which share the lhs in the
+  // XCD's L2; with few row tiles a single tile.
+  const int n_mtiles = __builtin_amdgcn_readfirstlane(pl.n_mtiles);
   const int X = P % 8 == 0 ? 8 : 1, x = blockIdx.x % X;
-  const int step_items = P / X, n_items = (int)((long long)all_items * (x + 1) / X);
-  const int first = (int)((long long)all_items * x / X) + blockIdx.x / X;
+  const int chunk = n_mtiles >= 4 * X ? n_ntiles : 1;
+  const int chunks = chunk == 1 ? n_mtiles * n_ntiles : n_mtiles;
+  const int n_items = (chunks - x + X - 1) / X * chunk;  // of this XCD
+  const int step_items = P / X, first = blockIdx.x / X;
+  auto tile_of = [&](int l) __attribute__((always_inline)) { return (x + X * (l / chunk)) * chunk + l % chunk; };
   const int NS = (K + C::BK - 1) / C::BK;
   constexpr int es = OUT_F32 ? 4 : 2;
 
   if (first < n_items) {
     // the current item and the workgroup's next one, found ahead of its turn
-    RowsItem it = decode_rows(pl, first, n_ntiles, N), it1 = it;
+    RowsItem it = decode_rows(pl, tile_of(first), n_ntiles, N), it1 = it;
     RowsSrc src = rows_src(p, it, w), src1 = src;
     int L = first, sc = 0, buf = 0;
     RowsWeights wa{}, wb{};
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
     rows_load_w(wa, src, 0, K, N, it.ncols - 64 * w, q, r16);
     rows_load_a(a, src, 0, K, tid);
     if (first + step_items < n_items) {
-      it1 = decode_rows(pl, first + step_items, n_ntiles, N);
+      it1 = decode_rows(pl, tile_of(first + step_items), n_ntiles, N);
       src1 = rows_src(p, it1, w);
     }
     rows_store_a(smem, a, tid);
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
       if (last) {
         L += step_items;
         if (L + step_items < n_items) {
-          it1 = decode_rows(pl, L + step_items, n_ntiles, N);
+          it1 = decode_rows(pl, tile_of(L + step_items), n_ntiles, N);
           src1 = rows_src(p, it1, w);
         }
       }

@@ -66,6 +66,8 @@ _handles = {}
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libgmm.so (raises when it is not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

@@ -262,3 +262,17 @@ def test_binding_refuses_host_tensors():
                   lambda: m.widen_mxfp4(x.to(torch.uint8), x)):
         with pytest.raises(m.GmmInvalid, match="device tensor"):
             call_()
+
+
+def test_binding_packs_the_c_struct():
+    """The packed bytes are the ctypes structure's, field by field."""
+    import torch
+
+    from moe_grouped_matrix_amd import _binding, _moe
+    s = _moe._TENSOR.pack(0x123450, 7, 3, 5, 6, 7, 0)
+    t = _binding.GmmTensor.from_buffer_copy(s)
+    assert (t.data, t.dtype, t.ndim, list(t.shape)) == (0x123450, 7, 3, [5, 6, 7, 0])
+    with pytest.raises(_binding.GmmInvalid, match="device tensor"):
+        _moe._pack(torch.zeros(2), "x", torch.device("cuda", 0))
+    with pytest.raises(_binding.GmmInvalid, match="device tensor"):
+        _moe._pack(None, "x", torch.device("cuda", 0))

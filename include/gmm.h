@@ -149,10 +149,9 @@ const char* gmm_last_error(const gmm_handle* h);
  *                microscaling encoding) is outside the contract.
  *                (BF16, F4E2M1) takes an E8M0 rhs_scale too (no lhs_scale):
  *                microscaled fp4 weights as gmm_quant_mxfp4_run of gmm_moe.h
- *                writes them, widened to bf16 with their scale.  Weights
- *                below the smallest normal bf16 (bytes 0 and 1) may count as
- *                zero, and those past the largest (bytes 253 and 254) become
- *                infinities; byte 255 makes its block NaN.
+ *                writes them, widened to bf16 with their scale: exact for
+ *                bytes 0 .. 252.  Weights past the largest bf16 (bytes 253
+ *                and 254) become infinities; byte 255 makes its block NaN.
  *   group_offset NULL (s = 0) or a device pointer to one int32 s.
  *   out          [M,N], F32 or BF16.  All M rows are written.  out must not
  *                overlap any input.

@@ -149,20 +149,20 @@ def handle(device: Union[int, torch.device, None] = None):
     return h
 
 
-def _view(t: Optional[torch.Tensor], name: str, dtypes=_DTYPE):
+def _view(t: Optional[torch.Tensor], name: str):
     if t is None:
         return None
     if not t.is_cuda:
         raise GmmInvalid(GMM_E_INVALID, f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise GmmInvalid(GMM_E_INVALID, f"{name} must be contiguous")
-    if t.dtype not in dtypes:
+    if t.dtype not in _DTYPE:
         raise GmmInvalid(GMM_E_INVALID, f"{name}: unsupported dtype {t.dtype}")
     if t.dim() > 4:
         raise GmmInvalid(GMM_E_INVALID, f"{name}: more than 4 dimensions")
     v = GmmTensor()
     v.data = t.data_ptr() if t.numel() else None
-    v.dtype = dtypes[t.dtype]
+    v.dtype = _DTYPE[t.dtype]
     v.ndim = t.dim()
     for i, s in enumerate(t.shape):
         v.shape[i] = s
@@ -234,7 +234,10 @@ def gmm(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor, *,
     four-bit activations, lhs bytes [M,K/2].  Four-bit pairs: a bf16 lhs
     with any four-bit weight (widened to bf16); int4 / uint4 / int8 with
     int4 / uint4 / int8 (int8 products); fp4 e2m1 / e4m3fn / e5m2 with
-    fp4 e2m1 / e4m3fn / e5m2 (the f8f6f4 products)."""
+    fp4 e2m1 / e4m3fn / e5m2 (the f8f6f4 products).  Microscaled operands
+    (blocks of 32 along K, float8_e8m0fnu scales as quant_mxfp4() writes
+    them): the f8f6f4 pairs with either scale, and a bf16 lhs with
+    "fp4_e2m1" weights and an rhs_scale."""
     lib = load()
     dev = lhs.device
     h = handle(dev)

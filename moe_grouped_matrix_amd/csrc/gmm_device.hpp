@@ -246,8 +246,9 @@ __device__ inline i32x4 nib8_to_bf16x8(unsigned w) {
 // conversions take it (they read the exponent alone: byte 0 is 2^-127).
 __device__ __forceinline__ float e8m0_operand(int byte) { return __int_as_float(byte << 23); }
 
-// 8 fp4 e2m1 values (as nib8_to_bf16x8) times 2^(byte - 127), exact while the
-// products are normal bf16 values (bytes 2 .. 252).
+// 8 fp4 e2m1 values (as nib8_to_bf16x8) times 2^(byte - 127): exact in bf16
+// (subnormals included) up to byte 252, infinities where a product passes
+// the largest bf16, NaN for byte 255 (checked for every byte and code).
 __device__ __forceinline__ i32x4 fp4x8_scaled_bf16(unsigned w, int byte) {
   const float s = e8m0_operand(byte);
   i32x4 r;
@@ -325,8 +326,6 @@ struct Cfg {
   static constexpr int LDS = 2 * (A_BYTES + B_BYTES);
   static constexpr int BSB = B_FP8 ? 1 : ES;  // rhs storage bytes per element (four-bit: half)
   static constexpr bool B_NIB = B_FP8 && FB >= 3;  // four-bit weights widened to bf16
-  static constexpr bool MXI = MX_ && OP == Op::FP8;  // block scales on the instruction
-  static constexpr bool MXW = MX_ && B_FP8;          // the weight's block scales in the widening
   // four-bit operands of a one-byte product (fp4 e2m1 on the f8f6f4
   // instruction as it is; int4 / uint4 widened to int8 in LDS): a K step of
   // 128 elements is 64 bytes of a row, loaded 8 bytes a chunk
@@ -350,8 +349,7 @@ struct Cfg {
   static_assert(OP != Op::I8 || ((FA == 0 || FA == 3 || FA == 4) && (FB == 0 || FB == 3 || FB == 4)),
                 "int8 products: int8, int4 or uint4 operands");
   static_assert(!NN || OP != Op::I8, "NN needs f32 or bf16 weights");
-  static_assert(!MX || (!SCALED && (OP == Op::FP8 || (B_FP8 && FB == 5))),
-                "E8M0 block scales on the f8f6f4 instruction, or on widened fp4 weights");
+  static_assert(!MX || (OP == Op::FP8 && !SCALED), "E8M0 block scales on the f8f6f4 instruction");
 };
 
 // 16 nibbles (two words, the low nibble of each byte first) widened to 16
@@ -423,11 +421,9 @@ struct Stage {
   i32x4 b[C::B_CH];
 };
 
-// sr: the weight's E8M0 block scales from column n0 (MXW only).
 template <class C>
 __device__ inline void load_tile(const C&, Stage<C>& st, __amdgpu_buffer_rsrc_t ar,
-                                 __amdgpu_buffer_rsrc_t br, __amdgpu_buffer_rsrc_t sr, int kt, int K, int N,
-                                 int n0) {
+                                 __amdgpu_buffer_rsrc_t br, int kt, int K, int N, int n0) {
   const int tid = threadIdx.x;
   const int arow_bytes = K * C::ES;
 #pragma unroll
@@ -451,8 +447,7 @@ __device__ inline void load_tile(const C&, Stage<C>& st, __amdgpu_buffer_rsrc_t 
         st.b[i] = i32x4{v[0], v[1], 0, 0};
       } else if constexpr (C::B_NIB) {
         st.b[i][0] = __builtin_amdgcn_raw_buffer_load_b32(br, r * (K / 2) + kt * 32 + cc * 4, 0, 0);
-        // MXW: chunk cc holds K elements [64 kt + 8 cc, + 8), in block 2 kt + cc / 4
-        st.b[i][1] = C::MXW ? (int)__builtin_amdgcn_raw_buffer_load_b8(sr, (2 * kt + (cc >> 2)) * N + r, 0, 0) : 0;
+        st.b[i][1] = 0;
       } else if constexpr (C::B_FP8) {
         i32x2 v = __builtin_amdgcn_raw_buffer_load_b64(br, r * K + kt * 64 + cc * 8, 0, 0);
         st.b[i][0] = v[0];
@@ -502,9 +497,7 @@ __device__ inline void store_tile(const C&, const Stage<C>& st, char* sa, char* 
     for (int i = 0; i < C::B_CH; ++i) {
       const int c = tid + i * C::T;
       i32x4 v = st.b[i];
-      if constexpr (C::MXW)
-        v = fp4x8_scaled_bf16((unsigned)st.b[i][0], st.b[i][1]);
-      else if constexpr (C::B_NIB)
+      if constexpr (C::B_NIB)
         v = nib8_to_bf16x8<C::FB>((unsigned)st.b[i][0]);
       else if constexpr (C::B_FP8)
         v = fp8x8_to_bf16x8<C::FB>(i32x2{st.b[i][0], st.b[i][1]});
@@ -749,11 +742,7 @@ __global__ __launch_bounds__(C::T) void gmm_kernel(Params p) {
 
     const C cfg{};
     Stage<C> st;
-    __amdgpu_buffer_rsrc_t wsr = br;
-    if constexpr (C::MXW)
-      wsr = make_rsrc(reinterpret_cast<const uint8_t*>(p.rhs_scale) + (long long)h * p.nb * N + n0,
-                      (long long)(p.nb - 1) * N + ncols);
-    load_tile(cfg, st, ar, br, wsr, 0, K, N, n0);
+    load_tile(cfg, st, ar, br, 0, K, N, n0);
     store_tile(cfg, st, smem, smem + C::A_BYTES);
 
     // Block scales pass through LDS one block ahead, like the operands: in
@@ -797,15 +786,15 @@ __global__ __launch_bounds__(C::T) void gmm_kernel(Params p) {
     // rows and columns for K block 4 kt + q, one K step ahead in registers.
     // Rows and columns outside the tile read 0 (their outputs are dropped);
     // an absent scale is 127 (1.0).
-    constexpr int XA = C::MXI ? C::FM : 1, XB = C::MXI ? C::FN : 1;
+    constexpr int XA = C::MX ? C::FM : 1, XB = C::MX ? C::FN : 1;
     int sca[XA], scb[XB], nsca[XA], nscb[XB];
     const uint8_t* ls8 = reinterpret_cast<const uint8_t*>(p.lhs_scale);
     const uint8_t* rs8 = reinterpret_cast<const uint8_t*>(p.rhs_scale);
     const __amdgpu_buffer_rsrc_t lsr =
-        C::MXI && ls8 ? make_rsrc(ls8 + (long long)row0 * p.nb, (long long)rows * p.nb) : make_rsrc(p.lhs, 0);
+        C::MX && ls8 ? make_rsrc(ls8 + (long long)row0 * p.nb, (long long)rows * p.nb) : make_rsrc(p.lhs, 0);
     const __amdgpu_buffer_rsrc_t rsr =
-        C::MXI && rs8 ? make_rsrc(rs8 + (long long)h * p.nb * N + n0, (long long)(p.nb - 1) * N + ncols)
-                      : make_rsrc(p.lhs, 0);
+        C::MX && rs8 ? make_rsrc(rs8 + (long long)h * p.nb * N + n0, (long long)(p.nb - 1) * N + ncols)
+                     : make_rsrc(p.lhs, 0);
     auto load_mx = [&](int kt, int (&xa)[XA], int (&xb)[XB]) __attribute__((always_inline)) {
       const int b = kt * 4 + q;
 #pragma unroll
@@ -818,7 +807,7 @@ __global__ __launch_bounds__(C::T) void gmm_kernel(Params p) {
         xb[fn] = p.rhs_scale ? (int)__builtin_amdgcn_raw_buffer_load_b8(rsr, b * N + wn * C::TN + fn * 16 + r16, 0, 0)
                              : 127;
     };
-    if constexpr (C::MXI) load_mx(0, sca, scb);
+    if constexpr (C::MX) load_mx(0, sca, scb);
     __syncthreads();
 
     for (int kt = 0; kt < KT; ++kt) {
@@ -829,8 +818,8 @@ __global__ __launch_bounds__(C::T) void gmm_kernel(Params p) {
         next_scales = kt % kt_per_blk == 0 && kt / kt_per_blk + 1 < p.nb;
         if (next_scales) load_scales(kt / kt_per_blk + 1);
       }
-      if (kt + 1 < KT) load_tile(cfg, st, ar, br, wsr, kt + 1, K, N, n0);
-      if constexpr (C::MXI) {
+      if (kt + 1 < KT) load_tile(cfg, st, ar, br, kt + 1, K, N, n0);
+      if constexpr (C::MX) {
         if (kt + 1 < KT) load_mx(kt + 1, nsca, nscb);
         mma_tile_mx<C>(acc, sa, sb, sca, scb);
 #pragma unroll

@@ -16,6 +16,7 @@
 #include "gmm.h"
 #include "gmm_handle.hpp"
 #include "gmm_launch.hpp"
+#include "gmm_mxw_launch.hpp"
 #include "gmm_tensor.hpp"
 
 using namespace gmmh;
@@ -200,8 +201,9 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
   }
   kc.scaled = !mx && (rhs_scale != nullptr || lhs_scale != nullptr);
   kc.mx = mx;
+  // microscaled fp4 weights under a bf16 lhs (a kernel family of their own)
+  const bool weight_only = mx && kc.op == gmmk::Op::BF16 && rd == GMM_F4E2M1;
   if (mx) {
-    const bool weight_only = kc.op == gmmk::Op::BF16 && rd == GMM_F4E2M1;
     if (kc.op != gmmk::Op::FP8 && !weight_only)
       return fail(h, GMM_E_UNSUPPORTED,
                   "E8M0 block scales need e4m3fn, e5m2 or fp4 e2m1 operands on both sides, or bf16 lhs and fp4 e2m1 rhs");
@@ -260,7 +262,7 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
     kc.size = gmmk::SizeClass::Small;
   else if (h->tile_policy == 2)
     kc.size = gmmk::SizeClass::Big;
-  else if (kc.mx && kc.op == gmmk::Op::BF16)
+  else if (weight_only)
     kc.size = gmmk::mxw_size(M, Ga);
   else
     kc.size = (M >= 8192 && M >= 512 * (Ga > 0 ? Ga : 1)) ? gmmk::SizeClass::Big : gmmk::SizeClass::Small;
@@ -288,7 +290,9 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
   p.out_f32 = out->dtype == GMM_F32;
 
   DeviceGuard g(h->device);
-  hipError_t e = gmmk::launch_gmm(p, kc, h->cu_count, static_cast<hipStream_t>(stream));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t e = weight_only ? gmmk::launch_mxw(p, kc.size, h->cu_count, kc.grid_cap, st)
+                                   : gmmk::launch_gmm(p, kc, h->cu_count, st);
   if (e != hipSuccess) return fail(h, GMM_E_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
   return GMM_OK;
 }

@@ -160,10 +160,6 @@ hipError_t launch_gmm(const Params& p, const KernelChoice& c, int cu, hipStream_
       return c.nn ? by_scaled<Op::F32, true, false>(p, c, cu, st)
                   : by_scaled<Op::F32, false, false>(p, c, cu, st);
     case Op::BF16:
-      if (c.mx) {  // fp4 weights with E8M0 block scales
-        if (c.nn || !c.b_fp8 || c.fmt != 5 << 3) return hipErrorInvalidValue;
-        return launch_mxw(p, c, cu, st);
-      }
       if (c.b_fp8) {  // widened weights: the rhs format in bits 3..5
         if (c.nn || (c.fmt & 7)) return hipErrorInvalidValue;
         switch (c.fmt >> 3) {

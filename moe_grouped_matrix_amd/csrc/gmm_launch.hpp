@@ -18,7 +18,7 @@ struct KernelChoice {
                 // 4 fp4 e2m1; I8 products: 0 int8, 3 int4, 4 uint4; widened bf16 weights
                 // (b_fp8): rhs 0 e4m3fn, 1 e5m2, 2 int8, 3 int4, 4 uint4, 5 fp4 e2m1
   bool scaled;  // f32 rhs_scale and/or lhs_scale present (folded per block)
-  bool mx;      // E8M0 scales of 32-element blocks, applied by the scaled instruction or the widening
+  bool mx;      // E8M0 scales of 32-element blocks, applied by the scaled instruction
   SizeClass size;
   int grid_cap;  // > 0: at most this many workgroups (a test hook)
 };
@@ -56,18 +56,6 @@ bool stream_fits(const Params& p);
 // Queue it for weight format fb (0 e4m3fn, 1 e5m2, 2 int8, 3 int4, 4 uint4,
 // 5 fp4 e2m1).
 hipError_t launch_stream(const Params& p, int fb, int cu_count, int grid_cap, hipStream_t stream);
-
-// The size class of a bf16 lhs with microscaled fp4 weights: the large-group
-// kernel's 256-row tiles pay from about 128 rows a group on (32 groups of 128
-// rows, 1408 x 1408: 29.5 us against 35.0 with the few-rows kernel; 128 of 64:
-// 80 against 71; 1 of 4096: 34 against 36; 8 of 256, 4096 x 4096: 104 against 95).
-inline SizeClass mxw_size(long long M, long long Ga) {
-  return M >= 4096 && M >= 128 * Ga ? SizeClass::Big : SizeClass::Small;
-}
-
-// Queue the product of a bf16 lhs with fp4 e2m1 weights and their E8M0 block
-// scales (gmm_mxw.hip).
-hipError_t launch_mxw(const Params& p, const KernelChoice& c, int cu_count, hipStream_t stream);
 
 // Queue the transposed grouped matmul (out [Ga,K,N]); grid_cap > 0 limits
 // the workgroups.

@@ -19,6 +19,7 @@
 #include <stdint.h>
 
 #include "gmm_device.hpp"
+#include "gmm_mx.hpp"
 #include "gmm_moe_launch.hpp"
 
 namespace gmmk {

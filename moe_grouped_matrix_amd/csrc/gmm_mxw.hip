@@ -7,8 +7,8 @@
 // sums: the products are plain bf16 ones with fp32 sums.
 #include <atomic>
 
-#include "gmm_launch.hpp"
 #include "gmm_mxw_big.hpp"
+#include "gmm_mxw_launch.hpp"
 #include "gmm_mxw_rows.hpp"
 
 namespace gmmk {
@@ -62,17 +62,17 @@ hipError_t launch_big(const Params& p, int cu, int cap, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_mxw(const Params& p, const KernelChoice& c, int cu, hipStream_t st) {
+hipError_t launch_mxw(const Params& p, SizeClass size, int cu, int cap, hipStream_t st) {
   // The large-group kernel runs a tile in steps of 64, three at least; below
   // that a product is its output's stores, and the few-rows kernel is the
   // faster one (131072 rows, K = 128, N = 1408: 184 us, 369 MB written).
-  if (c.size == SizeClass::Big && p.K >= 3 * 64) {
+  if (size == SizeClass::Big && p.K >= 3 * 64) {
     const bool bias = p.rhs_bias != nullptr;
     if (p.out_f32)
-      return bias ? launch_big<true, true>(p, cu, c.grid_cap, st) : launch_big<true, false>(p, cu, c.grid_cap, st);
-    return bias ? launch_big<false, true>(p, cu, c.grid_cap, st) : launch_big<false, false>(p, cu, c.grid_cap, st);
+      return bias ? launch_big<true, true>(p, cu, cap, st) : launch_big<true, false>(p, cu, cap, st);
+    return bias ? launch_big<false, true>(p, cu, cap, st) : launch_big<false, false>(p, cu, cap, st);
   }
-  return p.out_f32 ? launch_rows<true>(p, cu, c.grid_cap, st) : launch_rows<false>(p, cu, c.grid_cap, st);
+  return p.out_f32 ? launch_rows<true>(p, cu, cap, st) : launch_rows<false>(p, cu, cap, st);
 }
 
 }  // namespace gmmk

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "gmm_big.hpp"
+#include "gmm_mx.hpp"
 
 namespace gmmk {
 

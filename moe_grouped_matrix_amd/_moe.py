@@ -8,13 +8,12 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import struct
 from typing import Optional
 
 import torch
 
-from ._binding import (_DTYPE, _handles, _raise, GMM_E_INVALID, GMM_F4E2M1, GMM_I64, GmmInvalid, GmmTensor, handle,
-                       load)
+from ._binding import (_DTYPE, _PAD, _TENSOR, _handles, _raise, GMM_E_INVALID, GMM_F4E2M1, GMM_I64, GmmInvalid,
+                       handle, load)
 
 EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatch_run", "gmm_combine_run",
                 "gmm_combine_grad_run", "gmm_quant_mxfp4_run", "gmm_widen_mxfp4_run")
@@ -27,9 +26,6 @@ _PACKED_DTYPE = {torch.uint8: GMM_F4E2M1, torch.float4_e2m1fn_x2: GMM_F4E2M1}
 # host's share counts: a gmm_tensor is packed as the bytes of the C struct
 # (0.4 us against 1.5 us for a ctypes structure), and the current stream is
 # taken as the raw handle (0.1 us against 3 us for a Stream object).
-_TENSOR = struct.Struct("@Piiqqqq")
-assert _TENSOR.size == ctypes.sizeof(GmmTensor)
-_PAD = [(0,) * (4 - n) for n in range(5)]
 
 
 def _refuse(text: str):

@@ -19,9 +19,17 @@ namespace {
 // slots are cut into contiguous runs, one per workgroup; the first launch
 // counts every run's keys (kept key by key, so that a wave reads a key's counts
 // with one load a lane), and in the second each workgroup adds up the counts of
-// all runs (what stands before its own, and the totals) and ranks its slots.  Within a wave equal keys find each other by one ballot per key bit;
-// a wave takes 64 consecutive slots at a time, in order, so the rank of a slot
-// is its wave's running count plus the equal lanes below it.
+// all runs (what stands before its own, and the totals) and ranks its slots.
+// Within a wave equal keys find each other by one ballot per key bit; a wave
+// takes 64 consecutive slots at a time, in order, so the rank of a slot is its
+// wave's running count plus the equal lanes below it.  Up to 4096 slots one
+// workgroup does it all in one launch.
+//
+// Latency is what it costs: 3.0 us for one token's 8 slots, 6.7 us for 4096,
+// 3.4 + 8.9 us for 262144 slots of 128 experts (3 MB read and written, which a
+// copy moves in 1 us).  With the counts kept run by run and added with LDS
+// atomics the second launch took 13 us; read key by key, one key a wave at a
+// time, as much; eight keys a wave at a time 8.9 us.
 
 // Sum over the wave's lanes, by row shifts and row broadcasts (every lane gets
 // it; the order of the additions is fixed).
@@ -206,6 +214,14 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
 // is not a multiple of V ends in a chunk that starts V before its end and
 // overlaps the one before (both write the same values); rows narrower than V
 // go one element at a time.  Rows start at any multiple of the element size.
+//
+// 32768 tokens x top-8 of 128, 1408 bf16 columns, against a copy of as many
+// bytes (5.14 TB/s): dispatch 157 us (832 MB, 5.3 TB/s), combine 158 us (831 MB),
+// its gradient 312 us (1572 MB, 5.0 TB/s); counted HBM traffic 1.00 times those
+// bytes.  One row at a time and loads through the caches took 173, 180 and 374
+// us.  For a decode step of 256 tokens a lane takes one chunk, so that three
+// times the waves share the rows: dispatch 3.7 us (8.7 with a wave a token),
+// combine of f32 rows 4.4 us (13.9).
 
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 

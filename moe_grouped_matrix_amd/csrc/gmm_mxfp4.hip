@@ -15,6 +15,13 @@
 // takes 64 rows of one group (a contiguous run of codes while K is one panel)
 // and turns their scales around in LDS, so that they are written and read in
 // runs of 64 bytes.  An activation's scales [M, K/32] lie flat like the rest.
+// A lane takes eight elements: one 16-byte load of bf16, one word of codes.
+//
+// 128 x 1408 x 704 bf16 weights: quantised in 60 us (321 MB, 5.3 TB/s), widened
+// in 64 us (5.0 TB/s), a copy's rate (5.14 TB/s); counted HBM traffic is the
+// algorithmic one.  With scale bytes written where they belong one at a time,
+// and sixteen elements a lane, it was 78 and 94 us.  2048 x 1408 activations
+// take 3.4 and 3.3 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -14,9 +14,19 @@
 // 32 q + 8 i + [0, 8).  The lhs rows of a step, which all four waves need, pass
 // through a double-buffered LDS stage, loaded a step ahead into registers.  The
 // next step's loads (of this tile or the workgroup's next one) are in flight
-// while a step is multiplied.
+// while a step is multiplied.  In the result lane (q, r) holds row r and columns
+// 16 q + [0, 16).
 //
-// In the result lane (q, r) holds row r and columns 16 q + [0, 16).
+// 2048 rows of 128 experts, 1408 x 1408 (148 MB): 47 us, 3.1 TB/s; 16 rows in
+// every one of 128 groups of 4096 x 4096 (1.1 GB) 4.7 TB/s.  What bounds it: 5 us
+// pass before the first weight (launch, group sizes, plan); a bare read of the
+// same weights in the same pieces with a barrier a step takes 29 us; the rest is
+// the lhs, which every column tile reads again through the same L1, and the
+// products, which two waves a SIMD hide in part.  Tried on the way there: waves
+// that share out K and read the lhs straight from the L2, 62 us; steps of 128
+// (64-byte pieces of a line) 61 us with two to four workgroups a CU; weights two
+// or three steps ahead, the lhs two ahead, 512-column tiles of eight waves, no
+// gain; 64-row tiles spill (75 us).
 #pragma once
 
 #include "gmm_big.hpp"
@@ -153,23 +163,20 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
   const int M = p.M, N = p.N, K = p.K;
   const int P = gridDim.x, slot = xcd_slot(blockIdx.x, P);  // (of the fill)
   const int n_ntiles = (N + C::BN - 1) / C::BN;
-  // XCD x takes chunks x, x + 8, ... of the tiles, its workgroups in turn: as
-  // many tiles on every XCD, and a popular expert's full tiles spread over all.
-  // A chunk is a row tile with all its column tiles, which share the lhs in the
-  // XCD's L2; with few row tiles a single tile.
-  const int n_mtiles = __builtin_amdgcn_readfirstlane(pl.n_mtiles);
+  // Every XCD gets a contiguous eighth of the tiles (they share lhs rows and,
+  // in groups of more than one row tile, weights in its L2), which its
+  // workgroups take in turn.  Whole rounds over the grid left the last round to
+  // some XCDs only: 50 against 40 us for 768 tiles on 512 workgroups.
+  const int all_items = __builtin_amdgcn_readfirstlane(pl.n_mtiles) * n_ntiles;
   const int X = P % 8 == 0 ? 8 : 1, x = blockIdx.x % X;
-  const int chunk = n_mtiles >= 4 * X ? n_ntiles : 1;
-  const int chunks = chunk == 1 ? n_mtiles * n_ntiles : n_mtiles;
-  const int n_items = (chunks - x + X - 1) / X * chunk;  // of this XCD
-  const int step_items = P / X, first = blockIdx.x / X;
-  auto tile_of = [&](int l) __attribute__((always_inline)) { return (x + X * (l / chunk)) * chunk + l % chunk; };
+  const int step_items = P / X, n_items = (int)((long long)all_items * (x + 1) / X);
+  const int first = (int)((long long)all_items * x / X) + blockIdx.x / X;
   const int NS = (K + C::BK - 1) / C::BK;
   constexpr int es = OUT_F32 ? 4 : 2;
 
   if (first < n_items) {
     // the current item and the workgroup's next one, found ahead of its turn
-    RowsItem it = decode_rows(pl, tile_of(first), n_ntiles, N), it1 = it;
+    RowsItem it = decode_rows(pl, first, n_ntiles, N), it1 = it;
     RowsSrc src = rows_src(p, it, w), src1 = src;
     int L = first, sc = 0, buf = 0;
     RowsWeights wa{}, wb{};
@@ -177,7 +184,7 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
     rows_load_w(wa, src, 0, K, N, it.ncols - 64 * w, q, r16);
     rows_load_a(a, src, 0, K, tid);
     if (first + step_items < n_items) {
-      it1 = decode_rows(pl, tile_of(first + step_items), n_ntiles, N);
+      it1 = decode_rows(pl, first + step_items, n_ntiles, N);
       src1 = rows_src(p, it1, w);
     }
     rows_store_a(smem, a, tid);
@@ -210,7 +217,7 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
       if (last) {
         L += step_items;
         if (L + step_items < n_items) {
-          it1 = decode_rows(pl, tile_of(L + step_items), n_ntiles, N);
+          it1 = decode_rows(pl, L + step_items, n_ntiles, N);
           src1 = rows_src(p, it1, w);
         }
       }

@@ -1,7 +1,7 @@
 """Grouped matrix multiplication (gmm) for AMD MI355X (gfx950).
 
 The computation runs in hand-written HIP kernels behind the C ABI of
-libgmm.so (include/gmm.h); this package is the thin Python binding over it.
+libgmm.so (include/gmm.h, include/gmm_moe.h); this package is the thin Python binding over it.
 Build the library with ``moe_grouped_matrix_amd.build.build()``."""
 from ._binding import (EXPORTED, FLAG_BAD_OFFSET, FLAG_NEGATIVE_SIZE, FLAG_SCHEDULE_TIMEOUT,  # noqa: F401
                        FLAG_SIZES_EXCEED_M,

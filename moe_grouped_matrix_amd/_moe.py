@@ -3,18 +3,22 @@ expert, dispatched into expert rows and combined back, with gradients, and
 microscaled fp4 tensors.
 
 Argument marshalling only, as in _binding.py: the checks and the computation
-are the library's."""
+are the library's.  The common call (outputs to be made, the current stream)
+is marshalled by compiled host code, _moe_ext.so; every other one here."""
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 from typing import Optional
 
 import torch
 
 from ._binding import (_DTYPE, _PAD, _TENSOR, _handles, _raise, GMM_E_INVALID, GMM_F4E2M1, GMM_I64, GmmInvalid,
-                       handle, load)
+                       LIB_PATH, handle, load)
 
+# in the order of _moe_ext's bind()
 EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatch_run", "gmm_combine_run",
                 "gmm_combine_grad_run", "gmm_quant_mxfp4_run", "gmm_widen_mxfp4_run")
 FLAG_BAD_ROW = 0x10
@@ -23,9 +27,32 @@ _ID_DTYPE = {torch.int32: _DTYPE[torch.int32], torch.int64: GMM_I64}
 _PACKED_DTYPE = {torch.uint8: GMM_F4E2M1, torch.float4_e2m1fn_x2: GMM_F4E2M1}
 
 # These calls take a few microseconds on the GPU for a decode step, so the
-# host's share counts: a gmm_tensor is packed as the bytes of the C struct
-# (0.4 us against 1.5 us for a ctypes structure), and the current stream is
-# taken as the raw handle (0.1 us against 3 us for a Stream object).
+# host's share counts.  _moe_ext does the common call without a Python step in
+# between; it returns None for every other one, and for a refused one, which
+# then goes the long way below and is told why.
+EXT_PATH = os.path.join(os.path.dirname(LIB_PATH), "_moe_ext.so")
+_ext = None
+
+
+def _load_ext():
+    global _ext
+    lib = load()
+    if not os.path.exists(EXT_PATH):
+        raise ImportError(f"{EXT_PATH} is not built; run moe_grouped_matrix_amd.build.build()")
+    spec = importlib.util.spec_from_file_location("_moe_ext", EXT_PATH)
+    ext = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ext)
+    ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
+    for dev, h in _handles.items():
+        ext.set_handle(dev, h)
+    _ext = ext
+    return ext
+
+
+def _current(t) -> int:
+    """The raw current stream of a device tensor's device (0 otherwise)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
 
 
 def _refuse(text: str):
@@ -114,10 +141,11 @@ def _run(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], inputs, *ar
         _refuse(f"the stream is on {stream.device}, the tensors on {dev}")
     else:
         raw = stream.cuda_stream
-    h = _handles.get(dev.index) or handle(dev)
+    h = handle(dev)
     status = fn(h, *args, raw)
     if status:
         _raise(status, h)
+    (_ext or _load_ext()).set_handle(dev.index, h)
     if stream is not None:
         for t in inputs:
             if t is not None:
@@ -143,6 +171,10 @@ def sort_tokens(expert_ids: torch.Tensor, num_groups: int, *,
     [T,k], each slot's row in the sorted order).  An id outside [0, num_groups)
     leaves its slot unrouted: its row comes after all others, and slot_row
     holds the row's bitwise complement (a negative number)."""
+    if group_sizes is None and slot_row is None and stream is None:
+        made = (_ext or _load_ext()).sort_tokens(expert_ids, int(num_groups), _current(expert_ids))
+        if made is not None:
+            return made
     dev = _device(expert_ids, "expert_ids")
     ids = _pack(expert_ids, "expert_ids", dev, _ID_DTYPE)
     groups = int(num_groups)
@@ -162,6 +194,10 @@ def dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, out: Optional[torch.Ten
     rows[slot_row[t,j]] = x[t], the rows of unrouted slots zeros.  x [T,D] of
     any one-, two- or four-byte dtype, slot_row from sort_tokens(); returns
     rows [T*k,D], the lhs of gmm().  The gradient is combine(drows, slot_row)."""
+    if out is None and stream is None:
+        made = (_ext or _load_ext()).dispatch(x, slot_row, _current(x))
+        if made is not None:
+            return made
     dev = _device(x, "x")
     xv, sv = _pack(x, "x", dev), _pack(slot_row, "slot_row", dev)
     out, ov = _out(out, "out", (slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype, dev, stream)
@@ -177,6 +213,11 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.
     float32, rounded once.  rows [T*k,D] and weights [T,k] float32 or bfloat16
     (weights None: all 1, the gradient of dispatch()); returns out [T,D] of
     out_dtype (rows' dtype by default)."""
+    if out is None and stream is None:
+        made = (_ext or _load_ext()).combine(rows, slot_row, weights,
+                                             -1 if out_dtype is None else _DTYPE.get(out_dtype, -2), _current(rows))
+        if made is not None:
+            return made
     dev = _device(rows, "rows")
     rv, sv = _pack(rows, "rows", dev), _pack(slot_row, "slot_row", dev)
     wv = _pack(weights, "weights", dev) if weights is not None else None
@@ -192,6 +233,10 @@ def combine_grad(dout: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
     """The gradients of combine() with weights, through libgmm.so
     (gmm_combine_grad_run).  Returns (drows [T*k,D] of rows' dtype, zeros in
     the rows of unrouted slots; dweights [T,k] of weights' dtype, 0 there)."""
+    if drows is None and dweights is None and stream is None:
+        made = (_ext or _load_ext()).combine_grad(dout, rows, slot_row, weights, _current(dout))
+        if made is not None:
+            return made
     dev = _device(dout, "dout")
     if weights is None:
         _refuse("weights are required (without them the gradient is dispatch())")
@@ -203,11 +248,14 @@ def combine_grad(dout: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
     return drows, dweights
 
 
+_RANK = {"lhs": 2, "rhs": 3}
+
+
 def _operand(operand: str, dims: int, name: str) -> None:
-    if operand not in ("lhs", "rhs"):
+    if operand not in _RANK:
         _refuse(f"operand must be 'lhs' or 'rhs', got {operand!r}")
-    if dims != (2 if operand == "lhs" else 3):
-        _refuse(f"{name}: a {operand} is a {2 if operand == 'lhs' else 3}-tensor")
+    if dims != _RANK[operand]:
+        _refuse(f"{name}: a {operand} is a {_RANK[operand]}-tensor")
 
 
 def quant_mxfp4(x: torch.Tensor, *, operand: str = "lhs", q: Optional[torch.Tensor] = None,
@@ -218,6 +266,10 @@ def quant_mxfp4(x: torch.Tensor, *, operand: str = "lhs", q: Optional[torch.Tens
     layouts that gmm() takes: operand "lhs" x [M,K] -> scale [M,K/32] (with
     lhs_format="fp4_e2m1"), "rhs" x [Ga,N,K] -> scale [Ga,K/32,1,N] (with
     rhs_format="fp4_e2m1")."""
+    if q is None and scale is None and stream is None and operand in _RANK:
+        made = (_ext or _load_ext()).quant_mxfp4(x, _RANK[operand], _current(x))
+        if made is not None:
+            return made
     dev = _device(x, "x")
     _operand(operand, x.dim(), "x")
     xv = _pack(x, "x", dev)
@@ -236,6 +288,10 @@ def widen_mxfp4(q: torch.Tensor, scale: torch.Tensor, *, operand: str = "lhs",
     """The values of a microscaled fp4 tensor through libgmm.so
     (gmm_widen_mxfp4_run), exact in bfloat16 and float32: q and scale as
     quant_mxfp4() returns them for the same operand; returns [...,K]."""
+    if out is None and stream is None and operand in _RANK:
+        made = (_ext or _load_ext()).widen_mxfp4(q, scale, _RANK[operand], _DTYPE.get(out_dtype, -2), _current(q))
+        if made is not None:
+            return made
     dev = _device(q, "q")
     _operand(operand, q.dim(), "q")
     qv, sv = _pack(q, "q", dev, _PACKED_DTYPE), _pack(scale, "scale", dev)

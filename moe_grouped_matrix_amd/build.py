@@ -1,7 +1,8 @@
-"""Build libgmm.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libgmm.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_moe_ext.so (host code) beside it with the C++ compiler.
 
 Run ``python -m moe_grouped_matrix_amd.build`` or call ``build()``; the
-library is written next to this file."""
+libraries are written next to this file."""
 from __future__ import annotations
 
 import os
@@ -12,6 +13,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmm.so")
+EXT = os.path.join(HERE, "_moe_ext.so")  # the Python side of gmm_moe.h (host code over torch's C++ API)
 SOURCES = [os.path.join(CSRC, n) for n in
            ("gmm_kernels.hip", "gmm_w8a8.hip", "gmm_stream.hip", "gmm_quant.hip", "gmm_moe.hip", "gmm_mxfp4.hip", "gmm_mxw.hip",
             "gmm_api.cpp", "gmm_moe_api.cpp")]
@@ -35,6 +37,19 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def _ext_command(out: str):
+    """Compile and link csrc/moe_ext.cpp against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [sysconfig.get_paths()["include"], os.path.join(HERE, "..", "include")] + cpp_extension.include_paths()
+    return ([os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi())] + ["-I" + i for i in inc] +
+            [os.path.join(CSRC, "moe_ext.cpp"), "-o", out, "-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch_python"])
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -55,6 +70,9 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
         objs.append(obj)
+    ext = EXT + tag
+    cmd = _ext_command(ext)
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     errors = []
     for cmd, pr in procs:
         out, err = pr.communicate()
@@ -62,12 +80,13 @@ def build(verbose: bool = False) -> str:
             errors.append(" ".join(cmd) + "\n" + out + err)
     try:
         if errors:
-            raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
+            raise RuntimeError("compiling failed:\n" + "\n".join(errors))
         tmp = LIB + tag
         _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
         os.replace(tmp, LIB)
+        os.replace(ext, EXT)
     finally:
-        for o in objs:
+        for o in objs + [ext]:
             if os.path.exists(o):
                 os.remove(o)
     return LIB

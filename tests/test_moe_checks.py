@@ -264,6 +264,29 @@ def test_binding_refuses_host_tensors():
             call_()
 
 
+def test_the_compiled_binding_leaves_what_it_does_not_take():
+    """Without a device every call comes back as None (the long way refuses it),
+    and a wrong number of arguments is an error."""
+    import torch
+
+    import moe_grouped_matrix_amd as m
+    from moe_grouped_matrix_amd import _moe
+    m.load()
+    ext = _moe._load_ext()
+    ids, x = torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 64, dtype=torch.bfloat16)
+    slots = torch.zeros(4, 2, dtype=torch.int32)
+    assert ext.sort_tokens(ids, 4, 0) is None and ext.sort_tokens(None, 4, 0) is None
+    assert ext.dispatch(x, slots, 0) is None and ext.dispatch(x, "slots", 0) is None
+    assert ext.combine(x, slots, None, -1, 0) is None
+    assert ext.combine_grad(x, x, slots, None, 0) is None
+    assert ext.quant_mxfp4(x, 2, 0) is None and ext.widen_mxfp4(x, x, 2, 1, 0) is None
+    assert ext.sort_tokens(ids, "four", 0) is None and ext.sort_tokens(ids, 1 << 70, 0) is None
+    for call_ in (lambda: ext.dispatch(x), lambda: ext.bind(1), lambda: ext.set_handle(0)):
+        with pytest.raises(TypeError):
+            call_()
+    assert m.EXPORTED_MOE[0] == "gmm_sort_tokens_workspace" and len(m.EXPORTED_MOE) == 7
+
+
 def test_binding_packs_the_c_struct():
     """The packed bytes are the ctypes structure's, field by field."""
     import torch

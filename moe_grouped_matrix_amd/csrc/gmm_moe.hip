@@ -25,23 +25,25 @@ namespace {
 // wave's running count plus the equal lanes below it.  Up to 4096 slots one
 // workgroup does it all in one launch.
 //
-// Latency is what it costs: 3.0 us for one token's 8 slots, 6.7 us for 4096,
-// 3.4 + 8.9 us for 262144 slots of 128 experts (3 MB read and written, which a
+// Latency is what it costs: 2.9 us for one token's 8 slots, 5.9 us for 4096,
+// 3.4 + 7.9 us for 262144 slots of 128 experts (3 MB read and written, which a
 // copy moves in 1 us).  With the counts kept run by run and added with LDS
-// atomics the second launch took 13 us; read key by key, one key a wave at a
-// time, as much; eight keys a wave at a time 8.9 us.
+// atomics the second launch took 13 us, and so it did read key by key, one key a
+// wave at a time; eight keys a wave at a time 8.9 us; the ids asked for before
+// the counts are waited for, and the scan of the keys in lane shifts, 7.9 us.
 
-// Sum over the wave's lanes, by row shifts and row broadcasts (every lane gets
-// it; the order of the additions is fixed).
-__device__ __forceinline__ int wave_sum(int v) {
+// Inclusive prefix sum and sum over the wave's lanes, by row shifts and row
+// broadcasts (the order of the additions is fixed).
+__device__ __forceinline__ int wave_incl_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return __builtin_amdgcn_readlane(v, 63);
+  return v;
 }
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_incl_scan(v), 63); }
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_f32(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
@@ -81,13 +83,24 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
   __shared__ int cnt[W * (kMaxGroups + 1)];
   __shared__ int base[kMaxGroups + 1];   // per key: the row of the workgroup's next slot
   __shared__ int total[kMaxGroups + 1];  // per key: all slots
-  __shared__ long long wave_tot[W];
+  __shared__ int wave_tot[W];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int S = p.G + 1;
   const bool alone = gridDim.x == 1;
   const int bits = 32 - __builtin_clz(p.G);  // keys 0 .. G
   const long long lo = blockIdx.x * p.per, hi = lo + p.per < p.n ? lo + p.per : p.n;
 
+  // the first round's keys are asked for before the counts are waited for
+  int key[ITEMS];
+  auto load_keys = [&](long long r0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const long long s = r0 + w * (64 * ITEMS) + i * 64 + lane;
+      key[i] = s < hi ? sort_key(p, s) : -1;
+    }
+  };
+  load_keys(lo);
+  for (int i = tid; i < W * S; i += T) cnt[i] = 0;
   if (alone) {
     for (int g = tid; g < S; g += T) base[g] = 0;
   } else {
@@ -123,15 +136,9 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
 
   bool first = true;
   for (long long r0 = lo; first || r0 < hi; r0 += T * ITEMS) {
-    for (int i = tid; i < W * S; i += T) cnt[i] = 0;
     __syncthreads();
-    int key[ITEMS], rank[ITEMS];
+    int rank[ITEMS];
     const long long w0 = r0 + w * (64 * ITEMS);
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const long long s = w0 + i * 64 + lane;
-      key[i] = s < hi ? sort_key(p, s) : -1;
-    }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       rank[i] = 0;
@@ -163,18 +170,27 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
         __syncthreads();
       }
       // keys tid*E .. of this thread: rows of smaller keys
-      long long sum = 0, all;
+      int sum = 0;
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (tid * E + e < p.G) sum += total[tid * E + e];
-      long long at = block_excl_scan<T>(sum, wave_tot, &all);
+      const int incl = wave_incl_scan(sum);
+      if (lane == 63) wave_tot[w] = incl;
+      __syncthreads();
+      int at = incl - sum, all = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int t = wave_tot[i];
+        at += i < w ? t : 0;
+        all += t;
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (tid * E + e < p.G) {
-          base[tid * E + e] += (int)at;
+          base[tid * E + e] += at;
           at += total[tid * E + e];
         }
-      if (tid == 0) base[p.G] += (int)all;
+      if (tid == 0) base[p.G] += all;
       if (blockIdx.x == 0)
         for (int g = tid; g < p.G; g += T) p.group_sizes[g] = total[g];
       __syncthreads();
@@ -199,8 +215,12 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
         p.slot_row[s] = key[i] < p.G ? row : ~row;
       }
     }
-    __syncthreads();
     first = false;
+    if (r0 + T * ITEMS < hi) {
+      load_keys(r0 + T * ITEMS);
+      __syncthreads();
+      for (int i = tid; i < W * S; i += T) cnt[i] = 0;
+    }
   }
 }
 

@@ -270,8 +270,9 @@ def test_the_compiled_binding_leaves_what_it_does_not_take():
     import torch
 
     import moe_grouped_matrix_amd as m
-    from moe_grouped_matrix_amd import _moe
-    m.load()
+    from moe_grouped_matrix_amd import _moe, build
+    if not os.path.exists(m.LIB_PATH) or not os.path.exists(_moe.EXT_PATH):
+        build.build()
     ext = _moe._load_ext()
     ids, x = torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 64, dtype=torch.bfloat16)
     slots = torch.zeros(4, 2, dtype=torch.int32)

@@ -494,8 +494,10 @@ __global__ __launch_bounds__(kRowT) void combine_grad_kernel(RowParams p) {
           for (int e = 0; e < V; ++e) {
             const float ge = to_f32(gv[u].v[e]);
             from_f32(w * ge, d.v[e]);
+            // (a select of the sum, not of a factor: 0 times an infinity would count)
             const bool count = !tail || at[u] + e >= (c0 + 64 * u + lane) * V;
-            dot = __builtin_fmaf(count ? ge : 0.f, to_f32(x[b][u].v[e]), dot);
+            const float sum = __builtin_fmaf(ge, to_f32(x[b][u].v[e]), dot);
+            dot = count ? sum : dot;
           }
           if (at[u] >= 0) store_vec(dst + at[u], d);
         }

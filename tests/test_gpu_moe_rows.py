@@ -193,6 +193,23 @@ def test_infinities_in_routed_rows_reach_the_sum():
     assert torch.equal(out.nan_to_num(nan=-1.0), want.nan_to_num(nan=-1.0))
 
 
+@pytest.mark.parametrize("D", [3, 8, 13, 517, 1027])
+def test_infinities_in_any_column_reach_the_gradient(D):
+    """One infinity a row, each column in turn: the product is that infinity
+    (not the NaN of an infinity times a zero), whatever the width."""
+    import moe_grouped_matrix_amd as m
+    slot_row = torch.arange(D, dtype=torch.int32).reshape(D, 1)
+    for dtype in (torch.float32, torch.bfloat16):
+        rows = torch.ones(D, D)
+        rows[torch.arange(D), torch.arange(D)] = float("inf") * (1 - 2 * (torch.arange(D) % 2)).float()
+        want = torch.diagonal(rows)[:, None]
+        print(f"infinite rows D={D} {dtype}", flush=True)
+        drows, dw = m.combine_grad(torch.ones(D, D).to(dtype).cuda(), rows.to(dtype).cuda(), slot_row.cuda(),
+                                   torch.ones(D, 1).cuda())
+        assert torch.equal(dw.cpu(), want)
+        assert bool((drows == 1).all())
+
+
 def test_bad_rows_are_flagged_and_write_nothing():
     import moe_grouped_matrix_amd as m
     T, k, D = 6, 2, 40

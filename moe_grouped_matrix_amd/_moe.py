@@ -24,6 +24,7 @@ EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatc
 FLAG_BAD_ROW = 0x10
 
 _ID_DTYPE = {torch.int32: _DTYPE[torch.int32], torch.int64: GMM_I64}
+_BYTE_DTYPE = {**_DTYPE, torch.uint8: _DTYPE[torch.int8]}  # rows that are only copied
 _PACKED_DTYPE = {torch.uint8: GMM_F4E2M1, torch.float4_e2m1fn_x2: GMM_F4E2M1}
 
 # These calls take a few microseconds on the GPU for a decode step, so the
@@ -180,9 +181,10 @@ def sort_tokens(expert_ids: torch.Tensor, num_groups: int, *,
     groups = int(num_groups)
     if group_sizes is not None and (group_sizes.dim() != 1 or group_sizes.numel() != groups):
         _refuse("group_sizes must hold num_groups elements")
-    group_sizes, gv = _out(group_sizes, "group_sizes", (max(groups, 0),), torch.int32, dev, stream)
+    # (a number past the limit of 1024 is refused by the run, whatever the output holds)
+    group_sizes, gv = _out(group_sizes, "group_sizes", (min(max(groups, 0), 1025),), torch.int32, dev, stream)
     slot_row, sv = _out(slot_row, "slot_row", expert_ids.shape, torch.int32, dev, stream)
-    need = _sort_workspace(expert_ids.numel(), groups)
+    need = _sort_workspace(expert_ids.numel(), group_sizes.numel())
     work = _empty((need,), torch.uint8, dev, stream) if need else None
     _run(load().gmm_sort_tokens_run, dev, stream, (expert_ids,), ids, gv, sv, work.data_ptr() if need else None, need)
     return group_sizes, slot_row
@@ -192,15 +194,17 @@ def dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, out: Optional[torch.Ten
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Tokens into expert rows through libgmm.so (gmm_dispatch_run):
     rows[slot_row[t,j]] = x[t], the rows of unrouted slots zeros.  x [T,D] of
-    any one-, two- or four-byte dtype, slot_row from sort_tokens(); returns
-    rows [T*k,D], the lhs of gmm().  The gradient is combine(drows, slot_row)."""
+    any dtype that gmm() takes, or uint8 (packed fp4 codes; their scales
+    [T,K/32] and quant()'s [T,K/128] go the same way), slot_row from
+    sort_tokens(); returns rows [T*k,D], the lhs of gmm().  The gradient is
+    combine(drows, slot_row)."""
     if out is None and stream is None:
         made = (_ext or _load_ext()).dispatch(x, slot_row, _current(x))
         if made is not None:
             return made
     dev = _device(x, "x")
-    xv, sv = _pack(x, "x", dev), _pack(slot_row, "slot_row", dev)
-    out, ov = _out(out, "out", (slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype, dev, stream)
+    xv, sv = _pack(x, "x", dev, _BYTE_DTYPE), _pack(slot_row, "slot_row", dev)
+    out, ov = _out(out, "out", (slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype, dev, stream, _BYTE_DTYPE)
     _run(load().gmm_dispatch_run, dev, stream, (x, slot_row), xv, sv, ov)
     return out
 

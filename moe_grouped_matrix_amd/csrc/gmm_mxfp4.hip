@@ -184,7 +184,7 @@ __device__ __forceinline__ unsigned div_small(unsigned u, unsigned magic) { retu
 
 template <bool F32>
 __global__ __launch_bounds__(kMxT) void quant_mxfp4_weight_kernel(Mxfp4Params p) {
-  __shared__ uint8_t sc[kMxPanel * kMxPitch];
+  __shared__ alignas(16) uint8_t sc[kMxPanel * kMxPitch];
   const long long tiles = mx_tiles(p);
   const int tid = threadIdx.x, N = p.rhs;
   const long long row_words = p.K / 8;
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kMxT) void widen_mxfp4_flat_kernel(Mxfp4Params p) {
 
 template <bool F32>
 __global__ __launch_bounds__(kMxT) void widen_mxfp4_weight_kernel(Mxfp4Params p) {
-  __shared__ uint8_t sc[kMxPanel * kMxPitch];
+  __shared__ alignas(16) uint8_t sc[kMxPanel * kMxPitch];
   const long long tiles = mx_tiles(p);
   const int tid = threadIdx.x, N = p.rhs;
   const long long row_words = p.K / 8;

@@ -140,7 +140,8 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Args x{a};
     const at::Tensor &t = x.tensor(0, 2), &slots = x.tensor(1, 2);
     if (!x.ok) return none();
-    const int code = code_of(t.scalar_type()), scode = code_of(slots.scalar_type());
+    // (bytes, packed fp4 codes among them, are only copied)
+    const int code = t.scalar_type() == at::kByte ? GMM_I8 : code_of(t.scalar_type()), scode = code_of(slots.scalar_type());
     if (code < 0 || scode < 0) return none();
     const at::Tensor out = at::empty({slots.numel(), t.size(1)}, t.options());
     const gmm_tensor xv = view(t, code), sv = view(slots, scode), ov = view(out, code);

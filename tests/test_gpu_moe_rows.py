@@ -104,6 +104,27 @@ def test_dispatch(T, k, D, unrouted):
         assert torch.equal(out.cpu().view(iv), want.view(iv))
 
 
+def test_dispatch_of_packed_codes():
+    """Codes and scales of quantised tokens go the way of the tokens."""
+    import moe_grouped_matrix_amd as m
+    x = torch.randn(37, 96, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    slot_row = _slots(37, 3, 5, 0.0).cuda()
+    q, s = m.quant_mxfp4(x)
+    wq, ws = m.quant_mxfp4(m.dispatch(x, slot_row))
+    rows, scales = m.dispatch(q, slot_row), m.dispatch(s, slot_row)
+    assert rows.dtype == torch.uint8 and torch.equal(rows, wq)
+    assert torch.equal(scales.view(torch.uint8), ws.view(torch.uint8))
+    assert torch.equal(m.dispatch(q, slot_row, out=torch.empty_like(wq)), wq)
+
+
+def test_more_groups_than_there_may_be_allocates_nothing_for_them():
+    import moe_grouped_matrix_amd as m
+    ids = torch.zeros(4, 2, dtype=torch.int64, device="cuda")
+    for groups in (1 << 45, 1 << 70):
+        with pytest.raises(m.GmmUnsupported):
+            m.sort_tokens(ids, groups)
+
+
 @pytest.mark.parametrize("unrouted", [0.0, 0.4])
 @pytest.mark.parametrize("T,k,D", ROWS)
 def test_combine(T, k, D, unrouted):

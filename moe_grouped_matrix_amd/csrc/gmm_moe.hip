@@ -237,7 +237,7 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
 //
 // 32768 tokens x top-8 of 128, 1408 bf16 columns, against a copy of as many
 // bytes (5.14 TB/s): dispatch 157 us (832 MB, 5.3 TB/s), combine 158 us (831 MB),
-// its gradient 312 us (1572 MB, 5.0 TB/s); counted HBM traffic 1.00 times those
+// its gradient 307 us (1572 MB, 5.1 TB/s); counted HBM traffic 1.00 times those
 // bytes.  One row at a time and loads through the caches took 173, 180 and 374
 // us.  For a decode step of 256 tokens a lane takes one chunk, so that three
 // times the waves share the rows: dispatch 3.7 us (8.7 with a wave a token),

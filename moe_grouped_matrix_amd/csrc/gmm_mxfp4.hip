@@ -27,6 +27,7 @@
 
 #include "gmm_device.hpp"
 #include "gmm_mx.hpp"
+#include "gmm_mx_tiles.hpp"
 #include "gmm_moe_launch.hpp"
 
 namespace gmmk {
@@ -35,8 +36,6 @@ namespace {
 
 constexpr int kMxT = 256;
 constexpr int kMxUnits = 4;    // units a thread has in flight
-constexpr int kMxRows = 64;    // rows of a weight tile
-constexpr int kMxPanel = 128;  // most blocks of K in a weight tile
 constexpr int kMxPitch = kMxRows + 4;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -151,33 +150,6 @@ __global__ __launch_bounds__(kMxT) void quant_mxfp4_flat_kernel(Mxfp4Params p) {
   }
 }
 
-// A weight tile: rows [64 t, 64 t + rows) of group g, blocks [b0, b0 + nb).
-struct MxTile {
-  long long row0;    // first row of all
-  long long scales;  // of (b0, the tile's first row) in [Ga, K/32, 1, N]
-  int rows, b0, nb;
-};
-
-__device__ __forceinline__ MxTile mx_tile(const Mxfp4Params& p, long long i) {
-  const int N = p.rhs, all = p.K / 32;
-  const int panels = (all + kMxPanel - 1) / kMxPanel, strips = (N + kMxRows - 1) / kMxRows;
-  MxTile t;
-  const long long s = i / panels;
-  t.b0 = (int)(i - s * panels) * kMxPanel;
-  t.nb = all - t.b0 < kMxPanel ? all - t.b0 : kMxPanel;
-  const long long g = s / strips;
-  const int n0 = (int)(s - g * strips) * kMxRows;
-  t.rows = N - n0 < kMxRows ? N - n0 : kMxRows;
-  t.row0 = g * N + n0;
-  t.scales = (g * all + t.b0) * N + n0;
-  return t;
-}
-
-__device__ __forceinline__ long long mx_tiles(const Mxfp4Params& p) {
-  const long long N = p.rhs, all = p.K / 32;
-  return p.rows / N * ((N + kMxRows - 1) / kMxRows) * ((all + kMxPanel - 1) / kMxPanel);
-}
-
 // u / d for u < 2^16, 2 <= d <= 2^9: magic = floor(2^32 / d) + 1 is off 2^32/d
 // by at most 1, times u below 2^32 / d.
 __device__ __forceinline__ unsigned div_small(unsigned u, unsigned magic) { return __umulhi(u, magic); }
@@ -185,11 +157,11 @@ __device__ __forceinline__ unsigned div_small(unsigned u, unsigned magic) { retu
 template <bool F32>
 __global__ __launch_bounds__(kMxT) void quant_mxfp4_weight_kernel(Mxfp4Params p) {
   __shared__ alignas(16) uint8_t sc[kMxPanel * kMxPitch];
-  const long long tiles = mx_tiles(p);
+  const long long tiles = mx_tiles(p.rows, p.rhs, p.K);
   const int tid = threadIdx.x, N = p.rhs;
   const long long row_words = p.K / 8;
   for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const MxTile t = mx_tile(p, i);
+    const MxTile t = mx_tile(p.rhs, p.K, i);
     const unsigned per = 4 * t.nb, units = t.rows * per;
     const unsigned magic = (unsigned)(0x100000000ull / per) + 1;
     for (unsigned u0 = tid; u0 < units; u0 += kMxT * kMxUnits) {
@@ -263,12 +235,12 @@ __global__ __launch_bounds__(kMxT) void widen_mxfp4_flat_kernel(Mxfp4Params p) {
 template <bool F32>
 __global__ __launch_bounds__(kMxT) void widen_mxfp4_weight_kernel(Mxfp4Params p) {
   __shared__ alignas(16) uint8_t sc[kMxPanel * kMxPitch];
-  const long long tiles = mx_tiles(p);
+  const long long tiles = mx_tiles(p.rows, p.rhs, p.K);
   const int tid = threadIdx.x, N = p.rhs;
   const long long row_words = p.K / 8;
   const unsigned* const q = static_cast<const unsigned*>(p.src);
   for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const MxTile t = mx_tile(p, i);
+    const MxTile t = mx_tile(p.rhs, p.K, i);
     for (int w = tid; w < t.nb * (kMxRows / 4); w += kMxT) {
       const int b = w / (kMxRows / 4), r = w % (kMxRows / 4) * 4;
       const uint8_t* const s = p.scale + t.scales + (long long)b * N + r;
@@ -308,8 +280,7 @@ unsigned flat_grid(long long units, int cu_count) {
 }
 
 unsigned weight_grid(const Mxfp4Params& p, int cu_count) {
-  const long long N = p.rhs, all = p.K / 32;
-  long long grid = p.rows / N * ((N + kMxRows - 1) / kMxRows) * ((all + kMxPanel - 1) / kMxPanel);
+  long long grid = mx_tiles(p.rows, p.rhs, p.K);
   const long long cap = (long long)cu_count * 8;
   if (grid > cap) grid = cap;
   return (unsigned)(grid < 1 ? 1 : grid);

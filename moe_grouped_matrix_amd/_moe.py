@@ -15,8 +15,8 @@ from typing import Optional
 
 import torch
 
-from ._binding import (_DTYPE, _PAD, _TENSOR, _handles, _raise, GMM_E_INVALID, GMM_F4E2M1, GMM_I64, GmmInvalid,
-                       LIB_PATH, handle, load)
+from ._binding import (_DTYPE, _PAD, _TENSOR, _empty, _handles, _raise, _raw_stream, _record, GMM_E_INVALID,
+                       GMM_F4E2M1, GMM_I64, GmmInvalid, LIB_PATH, handle, load)
 
 # in the order of _moe_ext's bind()
 EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatch_run", "gmm_combine_run",
@@ -105,22 +105,6 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-def _empty(shape, dtype: torch.dtype, dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """An output or workspace for a call on `stream` (None: the current one):
-    allocated on the stream that writes it, and kept from reuse while the
-    current stream may still read it."""
-    if stream is None:
-        if len(shape) == 2:  # (0.4 us less than torch.empty)
-            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=dev)
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-    current = torch.cuda.current_stream(dev)
-    if current != stream:
-        t.record_stream(current)
-    return t
-
-
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: torch.device,
          stream: Optional[torch.cuda.Stream], dtypes=_DTYPE):
     """The caller's output or a new one of this shape, and its C struct."""
@@ -136,21 +120,13 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: t
 def _run(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], inputs, *args) -> None:
     """The call itself.  On a stream of the caller's choice the inputs are kept
     from reuse until that stream has read them."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        _refuse(f"the stream is on {stream.device}, the tensors on {dev}")
-    else:
-        raw = stream.cuda_stream
+    raw = _raw_stream(stream, dev)
     h = handle(dev)
     status = fn(h, *args, raw)
     if status:
         _raise(status, h)
     (_ext or _load_ext()).set_handle(dev.index, h)
-    if stream is not None:
-        for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
+    _record(stream, inputs)
 
 
 @functools.lru_cache(maxsize=4096)

@@ -117,16 +117,17 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: t
     return t, _struct(t.data_ptr(), code, shape)
 
 
-def _run(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], inputs, *args) -> None:
-    """The call itself.  On a stream of the caller's choice the inputs are kept
-    from reuse until that stream has read them."""
+def _run(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], tensors, *args) -> None:
+    """The call itself.  On a stream of the caller's choice its tensors, the
+    caller's own outputs among them, are kept from reuse until that stream is
+    done with them."""
     raw = _raw_stream(stream, dev)
     h = handle(dev)
     status = fn(h, *args, raw)
     if status:
         _raise(status, h)
     (_ext or _load_ext()).set_handle(dev.index, h)
-    _record(stream, inputs)
+    _record(stream, tensors)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -162,7 +163,7 @@ def sort_tokens(expert_ids: torch.Tensor, num_groups: int, *,
     slot_row, sv = _out(slot_row, "slot_row", expert_ids.shape, torch.int32, dev, stream)
     need = _sort_workspace(expert_ids.numel(), group_sizes.numel())
     work = _empty((need,), torch.uint8, dev, stream) if need else None
-    _run(load().gmm_sort_tokens_run, dev, stream, (expert_ids,), ids, gv, sv, work.data_ptr() if need else None, need)
+    _run(load().gmm_sort_tokens_run, dev, stream, (expert_ids, group_sizes, slot_row), ids, gv, sv, work.data_ptr() if need else None, need)
     return group_sizes, slot_row
 
 
@@ -181,7 +182,7 @@ def dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, out: Optional[torch.Ten
     dev = _device(x, "x")
     xv, sv = _pack(x, "x", dev, _BYTE_DTYPE), _pack(slot_row, "slot_row", dev)
     out, ov = _out(out, "out", (slot_row.numel(), x.shape[1] if x.dim() == 2 else 0), x.dtype, dev, stream, _BYTE_DTYPE)
-    _run(load().gmm_dispatch_run, dev, stream, (x, slot_row), xv, sv, ov)
+    _run(load().gmm_dispatch_run, dev, stream, (x, slot_row, out), xv, sv, ov)
     return out
 
 
@@ -203,7 +204,7 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.
     wv = _pack(weights, "weights", dev) if weights is not None else None
     out, ov = _out(out, "out", (slot_row.shape[0], rows.shape[1] if rows.dim() == 2 else 0),
                    out_dtype if out_dtype is not None else rows.dtype, dev, stream)
-    _run(load().gmm_combine_run, dev, stream, (rows, slot_row, weights), rv, sv, wv, ov)
+    _run(load().gmm_combine_run, dev, stream, (rows, slot_row, weights, out), rv, sv, wv, ov)
     return out
 
 
@@ -224,7 +225,8 @@ def combine_grad(dout: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
                                            (weights, "weights"))]
     drows, rv = _out(drows, "drows", rows.shape, rows.dtype, dev, stream)
     dweights, wv = _out(dweights, "dweights", weights.shape, weights.dtype, dev, stream)
-    _run(load().gmm_combine_grad_run, dev, stream, (dout, rows, slot_row, weights), *views, rv, wv)
+    _run(load().gmm_combine_grad_run, dev, stream, (dout, rows, slot_row, weights, drows, dweights), *views, rv,
+         wv)
     return drows, dweights
 
 
@@ -258,7 +260,7 @@ def quant_mxfp4(x: torch.Tensor, *, operand: str = "lhs", q: Optional[torch.Tens
     q, qv = _out(q, "q", (*shape[:-1], K // 2), torch.uint8, dev, stream, _PACKED_DTYPE)
     scale, sv = _out(scale, "scale", (shape[0], K // 32) if operand == "lhs" else (shape[0], K // 32, 1, shape[1]),
                      torch.float8_e8m0fnu, dev, stream)
-    _run(load().gmm_quant_mxfp4_run, dev, stream, (x,), xv, qv, sv)
+    _run(load().gmm_quant_mxfp4_run, dev, stream, (x, q, scale), xv, qv, sv)
     return q, scale
 
 
@@ -276,5 +278,5 @@ def widen_mxfp4(q: torch.Tensor, scale: torch.Tensor, *, operand: str = "lhs",
     _operand(operand, q.dim(), "q")
     qv, sv = _pack(q, "q", dev, _PACKED_DTYPE), _pack(scale, "scale", dev)
     out, ov = _out(out, "out", (*q.shape[:-1], 2 * q.shape[-1]), out_dtype, dev, stream)
-    _run(load().gmm_widen_mxfp4_run, dev, stream, (q, scale), qv, sv, ov)
+    _run(load().gmm_widen_mxfp4_run, dev, stream, (q, scale, out), qv, sv, ov)
     return out

@@ -181,3 +181,33 @@ def test_a_stream_of_another_device_is_refused(streams):
         with pytest.raises(_binding.GmmInvalid, match="stream is on"):
             call()
     assert streams[2].raw == []
+
+
+def moe_calls():
+    """(name, call(stream, **given), inputs, {name of an output: the caller's}) of the token and fp4 operators."""
+    i32, f32, e8 = torch.int32, torch.float32, torch.float8_e8m0fnu
+    ids, slots, x = device(6, 2, dtype=torch.int64), device(6, 2, dtype=i32), device(6, 64)
+    rows, w = device(12, 64), device(6, 2, dtype=f32)
+    q, e = device(6, 32, dtype=torch.uint8), device(6, 2, dtype=e8)
+    return [
+        ("sort_tokens", lambda **kw: _moe.sort_tokens(ids, 4, **kw), (ids,),
+         dict(group_sizes=device(4, dtype=i32), slot_row=device(6, 2, dtype=i32))),
+        ("dispatch", lambda **kw: _moe.dispatch(x, slots, **kw), (x, slots), dict(out=device(12, 64))),
+        ("combine", lambda **kw: _moe.combine(rows, slots, w, **kw), (rows, slots, w), dict(out=device(6, 64))),
+        ("combine_grad", lambda **kw: _moe.combine_grad(x, rows, slots, w, **kw), (x, rows, slots, w),
+         dict(drows=device(12, 64), dweights=device(6, 2, dtype=f32))),
+        ("quant_mxfp4", lambda **kw: _moe.quant_mxfp4(x, **kw), (x,),
+         dict(q=device(6, 32, dtype=torch.uint8), scale=device(6, 2, dtype=e8))),
+        ("widen_mxfp4", lambda **kw: _moe.widen_mxfp4(q, e, **kw), (q, e), dict(out=device(6, 64))),
+    ]
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_token_and_fp4_operators(streams, i):
+    name, call, ins, _ = moe_calls()[i]
+    check(streams, lambda st: call(stream=st), ins)
+    name, call, ins, given = moe_calls()[i]
+    check(streams, lambda st: call(stream=st, **given), ins, tuple(given.values()))
+    name, call, ins, given = moe_calls()[i]
+    first = dict(list(given.items())[:1])
+    check(streams, lambda st: call(stream=st, **first), ins, tuple(first.values()))

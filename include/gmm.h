@@ -32,9 +32,10 @@
  *  - `stream` is a hipStream_t (NULL = the default stream).  gmm_run only
  *    queues work: it never synchronises and never copies group_sizes or the
  *    group offset to the host.
- *  - A handle is used by one host thread at a time.
+ *  - Several host threads may use a handle at once (gmm_destroy apart).
  *  - No exception crosses this boundary.  Every call returns a gmm_status;
- *    gmm_last_error() gives the text of the last failure on a handle.
+ *    gmm_last_error() gives the text of the calling thread's last failure on
+ *    a handle.
  */
 #ifndef GMM_MI355X_GMM_H
 #define GMM_MI355X_GMM_H
@@ -104,7 +105,8 @@ gmm_status gmm_create(gmm_handle** h, int device);
  * queued with the handle must have finished.  NULL is allowed. */
 gmm_status gmm_destroy(gmm_handle* h);
 
-/* gmm_last_error: text of the last failure on h ("" when none; never NULL). */
+/* gmm_last_error: text of the calling thread's last failure on h ("" when
+ * none; never NULL), good until that thread's next call on h. */
 const char* gmm_last_error(const gmm_handle* h);
 
 /*

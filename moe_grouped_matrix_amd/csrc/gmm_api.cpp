@@ -85,7 +85,7 @@ gmm_status gmm_destroy(gmm_handle* h) {
   return GMM_OK;
 }
 
-const char* gmm_last_error(const gmm_handle* h) { return h ? h->err.c_str() : "null handle"; }
+const char* gmm_last_error(const gmm_handle* h) { return h ? h->err.get() : "null handle"; }
 
 // Test hook: 0 chooses tiles from the problem shape, 1 forces the small
 // (decode) tiles, 2 the big tiles.  Results differ only in fp32 summation
@@ -258,9 +258,10 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
   if (M == 0) return GMM_OK;
 
   kc.grid_cap = h->grid_limit;
-  if (h->tile_policy == 1)
+  const int policy = h->tile_policy;
+  if (policy == 1)
     kc.size = gmmk::SizeClass::Small;
-  else if (h->tile_policy == 2)
+  else if (policy == 2)
     kc.size = gmmk::SizeClass::Big;
   else if (weight_only)
     kc.size = gmmk::mxw_size(M, Ga);
@@ -442,6 +443,7 @@ static gmm_status run_tgmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tenso
                                            static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(h, GMM_E_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
   } else {
+    std::lock_guard<std::mutex> lk(h->queues_mu);
     int32_t*& q = h->queues[stream];
     if (!q) {  // first call on this stream: its counters, zeroed
       if (hipMalloc(&q, kQueueBlock) != hipSuccess || hipMemset(q, 0, kQueueBlock) != hipSuccess) {

@@ -4,10 +4,42 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <map>
+#include <mutex>
 #include <string>
+#include <thread>
 
 #include "gmm.h"
+
+namespace gmmh {
+
+// The text of the last failure of every thread that used the handle.  A
+// thread's text is written by that thread alone, so the pointer that it gets
+// stays good until its own next call.
+class ErrorTexts {
+ public:
+  void clear() {
+    std::lock_guard<std::mutex> lk(mu_);
+    const auto it = text_.find(std::this_thread::get_id());
+    if (it != text_.end()) it->second.clear();
+  }
+  void set(const std::string& text) {
+    std::lock_guard<std::mutex> lk(mu_);
+    text_[std::this_thread::get_id()] = text;
+  }
+  const char* get() const {
+    std::lock_guard<std::mutex> lk(mu_);
+    const auto it = text_.find(std::this_thread::get_id());
+    return it != text_.end() ? it->second.c_str() : "";
+  }
+
+ private:
+  mutable std::mutex mu_;
+  std::map<std::thread::id, std::string> text_;
+};
+
+}  // namespace gmmh
 
 struct gmm_handle {
   int device = 0;
@@ -18,10 +50,11 @@ struct gmm_handle {
   // so each call finds its stream's counters reset by the previous one;
   // calls on different streams never share counters
   std::map<void*, int32_t*> queues;
-  int tile_policy = 0;        // 0 auto, 1 small tiles, 2 big tiles
-  int grid_limit = 0;         // > 0: at most this many workgroups per launch
-  void* scratch = nullptr;    // device address of the device's static scratch
-  std::string err;
+  std::mutex queues_mu;                // held while queues is looked at or added to
+  std::atomic<int> tile_policy{0};     // 0 auto, 1 small tiles, 2 big tiles
+  std::atomic<int> grid_limit{0};      // > 0: at most this many workgroups per launch
+  void* scratch = nullptr;             // device address of the device's static scratch
+  gmmh::ErrorTexts err;
 };
 
 namespace gmmh {
@@ -39,7 +72,7 @@ struct DeviceGuard {
 };
 
 inline gmm_status fail(gmm_handle* h, gmm_status st, const std::string& msg) {
-  if (h) h->err = msg;
+  if (h) h->err.set(msg);
   return st;
 }
 

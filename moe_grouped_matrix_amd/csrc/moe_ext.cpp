@@ -57,27 +57,50 @@ gmm_tensor view_packed(const at::Tensor& t) {
   return v;
 }
 
-// The arguments of one call.
+// The arguments of one call, read before the interpreter lock is let go.
 struct Args {
   PyObject* const* args;
   int dev = -1;
+  gmm_handle* handle = nullptr;
   bool ok = true;
 
   // A dense tensor of rank `dim` on the first one's device.
-  const at::Tensor& tensor(int i, int64_t dim) {
-    static const at::Tensor none;
+  at::Tensor tensor(int i, int64_t dim) {
     if (!ok || !THPVariable_Check(args[i])) {
       ok = false;
-      return none;
+      return {};
     }
-    const at::Tensor& t = THPVariable_Unpack(args[i]);
+    at::Tensor t = THPVariable_Unpack(args[i]);
     if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != dim || !t.is_contiguous()) ok = false;
-    if (ok && dev < 0) dev = t.get_device();
-    if (ok && (t.get_device() != dev || dev >= kDevices || !g_handles[dev])) ok = false;
+    if (ok && dev < 0) {
+      dev = t.get_device();
+      handle = dev < kDevices ? g_handles[dev] : nullptr;
+    }
+    if (ok && (t.get_device() != dev || !handle)) ok = false;
     return t;
   }
-  long long number(int i) { return PyLong_AsLongLong(args[i]); }
-  void* pointer(int i) { return PyLong_AsVoidPtr(args[i]); }
+  long long number(int i) {
+    const long long v = PyLong_AsLongLong(args[i]);
+    if (v == -1 && PyErr_Occurred()) ok = false;
+    return v;
+  }
+  void* pointer(int i) {
+    void* const v = PyLong_AsVoidPtr(args[i]);
+    if (!v && PyErr_Occurred()) ok = false;
+    return v;
+  }
+};
+
+// Lets other Python threads run while outputs are allocated and the call is
+// queued (the allocator and the launch may have to wait for the device).
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
 };
 
 PyObject* none() { Py_RETURN_NONE; }
@@ -118,19 +141,23 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, Body body) {
 PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&]() -> PyObject* {
     Args x{a};
-    const at::Tensor& ids = x.tensor(0, 2);
+    const at::Tensor ids = x.tensor(0, 2);
     const long long groups = x.number(1);
+    void* const stream = x.pointer(2);
     if (!x.ok || (ids.scalar_type() != at::kInt && ids.scalar_type() != at::kLong)) return none();
     size_t bytes = 0;
     if (g_entry.sort_workspace(ids.numel(), groups, &bytes) != GMM_OK) return none();
-    const at::Tensor sizes = at::empty({groups}, ids.options().dtype(at::kInt));
-    const at::Tensor slot_row = at::empty(ids.sizes(), ids.options().dtype(at::kInt));
-    at::Tensor work;
-    if (bytes) work = at::empty({(int64_t)bytes}, ids.options().dtype(at::kByte));
-    const gmm_tensor iv = view(ids, code_of(ids.scalar_type())), gv = view(sizes, GMM_I32), sv = view(slot_row, GMM_I32);
-    if (g_entry.sort(g_handles[x.dev], &iv, &gv, &sv, bytes ? work.mutable_data_ptr() : nullptr, bytes, x.pointer(2)))
-      return none();
-    return give(sizes, slot_row);
+    at::Tensor sizes, slot_row;
+    {
+      Unlocked u;
+      sizes = at::empty({groups}, ids.options().dtype(at::kInt));
+      slot_row = at::empty(ids.sizes(), ids.options().dtype(at::kInt));
+      at::Tensor work;
+      if (bytes) work = at::empty({(int64_t)bytes}, ids.options().dtype(at::kByte));
+      const gmm_tensor iv = view(ids, code_of(ids.scalar_type())), gv = view(sizes, GMM_I32), sv = view(slot_row, GMM_I32);
+      if (g_entry.sort(x.handle, &iv, &gv, &sv, bytes ? work.mutable_data_ptr() : nullptr, bytes, stream)) x.ok = false;
+    }
+    return x.ok ? give(sizes, slot_row) : none();
   });
 }
 
@@ -138,15 +165,20 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&]() -> PyObject* {
     Args x{a};
-    const at::Tensor &t = x.tensor(0, 2), &slots = x.tensor(1, 2);
+    const at::Tensor t = x.tensor(0, 2), slots = x.tensor(1, 2);
+    void* const stream = x.pointer(2);
     if (!x.ok) return none();
     // (bytes, packed fp4 codes among them, are only copied)
     const int code = t.scalar_type() == at::kByte ? GMM_I8 : code_of(t.scalar_type()), scode = code_of(slots.scalar_type());
     if (code < 0 || scode < 0) return none();
-    const at::Tensor out = at::empty({slots.numel(), t.size(1)}, t.options());
-    const gmm_tensor xv = view(t, code), sv = view(slots, scode), ov = view(out, code);
-    if (g_entry.dispatch(g_handles[x.dev], &xv, &sv, &ov, x.pointer(2))) return none();
-    return give(out);
+    at::Tensor out;
+    {
+      Unlocked u;
+      out = at::empty({slots.numel(), t.size(1)}, t.options());
+      const gmm_tensor xv = view(t, code), sv = view(slots, scode), ov = view(out, code);
+      if (g_entry.dispatch(x.handle, &xv, &sv, &ov, stream)) x.ok = false;
+    }
+    return x.ok ? give(out) : none();
   });
 }
 
@@ -154,23 +186,26 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     Args x{a};
-    const at::Tensor &rows = x.tensor(0, 2), &slots = x.tensor(1, 2);
+    const at::Tensor rows = x.tensor(0, 2), slots = x.tensor(1, 2);
     const bool weighted = a[2] != Py_None;
-    if (!x.ok) return none();
-    gmm_tensor wv{};
-    if (weighted) {
-      const at::Tensor& w = x.tensor(2, 2);
-      if (!x.ok) return none();
-      wv = view(w, code_of(w.scalar_type()));
-    }
-    const int code = code_of(rows.scalar_type());
+    at::Tensor w;
+    if (weighted) w = x.tensor(2, 2);
     const long long want = x.number(3);
+    void* const stream = x.pointer(4);
+    if (!x.ok) return none();
+    const int code = code_of(rows.scalar_type());
     if (code < 0 || (want != -1 && want != GMM_F32 && want != GMM_BF16)) return none();
     const at::ScalarType type = want == -1 ? rows.scalar_type() : want == GMM_F32 ? at::kFloat : at::kBFloat16;
-    const at::Tensor out = at::empty({slots.size(0), rows.size(1)}, rows.options().dtype(type));
-    const gmm_tensor rv = view(rows, code), sv = view(slots, code_of(slots.scalar_type())), ov = view(out, code_of(type));
-    if (g_entry.combine(g_handles[x.dev], &rv, &sv, weighted ? &wv : nullptr, &ov, x.pointer(4))) return none();
-    return give(out);
+    at::Tensor out;
+    {
+      Unlocked u;
+      out = at::empty({slots.size(0), rows.size(1)}, rows.options().dtype(type));
+      const gmm_tensor rv = view(rows, code), sv = view(slots, code_of(slots.scalar_type())), ov = view(out, code_of(type));
+      gmm_tensor wv{};
+      if (weighted) wv = view(w, code_of(w.scalar_type()));
+      if (g_entry.combine(x.handle, &rv, &sv, weighted ? &wv : nullptr, &ov, stream)) x.ok = false;
+    }
+    return x.ok ? give(out) : none();
   });
 }
 
@@ -178,16 +213,22 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     Args x{a};
-    const at::Tensor &dout = x.tensor(0, 2), &rows = x.tensor(1, 2), &slots = x.tensor(2, 2), &w = x.tensor(3, 2);
+    const at::Tensor dout = x.tensor(0, 2), rows = x.tensor(1, 2), slots = x.tensor(2, 2), w = x.tensor(3, 2);
+    void* const stream = x.pointer(4);
     if (!x.ok) return none();
     const int rcode = code_of(rows.scalar_type()), wcode = code_of(w.scalar_type());
     if (rcode < 0 || wcode < 0) return none();
-    const at::Tensor drows = at::empty(rows.sizes(), rows.options()), dw = at::empty(w.sizes(), w.options());
-    const gmm_tensor gv = view(dout, code_of(dout.scalar_type())), rv = view(rows, rcode);
-    const gmm_tensor sv = view(slots, code_of(slots.scalar_type())), wv = view(w, wcode);
-    const gmm_tensor ov = view(drows, rcode), dv = view(dw, wcode);
-    if (g_entry.combine_grad(g_handles[x.dev], &gv, &rv, &sv, &wv, &ov, &dv, x.pointer(4))) return none();
-    return give(drows, dw);
+    at::Tensor drows, dw;
+    {
+      Unlocked u;
+      drows = at::empty(rows.sizes(), rows.options());
+      dw = at::empty(w.sizes(), w.options());
+      const gmm_tensor gv = view(dout, code_of(dout.scalar_type())), rv = view(rows, rcode);
+      const gmm_tensor sv = view(slots, code_of(slots.scalar_type())), wv = view(w, wcode);
+      const gmm_tensor ov = view(drows, rcode), dv = view(dw, wcode);
+      if (g_entry.combine_grad(x.handle, &gv, &rv, &sv, &wv, &ov, &dv, stream)) x.ok = false;
+    }
+    return x.ok ? give(drows, dw) : none();
   });
 }
 
@@ -196,16 +237,20 @@ PyObject* quant_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&]() -> PyObject* {
     Args x{a};
     const long long dim = x.number(1);
-    const at::Tensor& t = x.tensor(0, dim);
+    const at::Tensor t = x.tensor(0, dim);
+    void* const stream = x.pointer(2);
     if (!x.ok || code_of(t.scalar_type()) < 0) return none();
     const int64_t K = t.size(dim - 1);
-    const auto q8 = t.options().dtype(at::kByte), e8 = t.options().dtype(at::kFloat8_e8m0fnu);
-    const at::Tensor q = dim == 2 ? at::empty({t.size(0), K / 2}, q8) : at::empty({t.size(0), t.size(1), K / 2}, q8);
-    const at::Tensor scale =
-        dim == 2 ? at::empty({t.size(0), K / 32}, e8) : at::empty({t.size(0), K / 32, 1, t.size(1)}, e8);
-    const gmm_tensor xv = view(t, code_of(t.scalar_type())), qv = view_packed(q), sv = view(scale, GMM_E8M0);
-    if (g_entry.quant(g_handles[x.dev], &xv, &qv, &sv, x.pointer(2))) return none();
-    return give(q, scale);
+    at::Tensor q, scale;
+    {
+      Unlocked u;
+      const auto q8 = t.options().dtype(at::kByte), e8 = t.options().dtype(at::kFloat8_e8m0fnu);
+      q = dim == 2 ? at::empty({t.size(0), K / 2}, q8) : at::empty({t.size(0), t.size(1), K / 2}, q8);
+      scale = dim == 2 ? at::empty({t.size(0), K / 32}, e8) : at::empty({t.size(0), K / 32, 1, t.size(1)}, e8);
+      const gmm_tensor xv = view(t, code_of(t.scalar_type())), qv = view_packed(q), sv = view(scale, GMM_E8M0);
+      if (g_entry.quant(x.handle, &xv, &qv, &sv, stream)) x.ok = false;
+    }
+    return x.ok ? give(q, scale) : none();
   });
 }
 
@@ -214,14 +259,19 @@ PyObject* widen_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     Args x{a};
     const long long dim = x.number(2), want = x.number(3);
-    const at::Tensor &q = x.tensor(0, dim), &scale = x.tensor(1, dim == 2 ? 2 : 4);
+    const at::Tensor q = x.tensor(0, dim), scale = x.tensor(1, dim == 2 ? 2 : 4);
+    void* const stream = x.pointer(4);
     if (!x.ok || q.scalar_type() != at::kByte || (want != GMM_F32 && want != GMM_BF16)) return none();
     std::vector<int64_t> shape(q.sizes().begin(), q.sizes().end());
     shape.back() *= 2;
-    const at::Tensor y = at::empty(shape, q.options().dtype(want == GMM_F32 ? at::kFloat : at::kBFloat16));
-    const gmm_tensor qv = view_packed(q), sv = view(scale, code_of(scale.scalar_type())), yv = view(y, (int)want);
-    if (g_entry.widen(g_handles[x.dev], &qv, &sv, &yv, x.pointer(4))) return none();
-    return give(y);
+    at::Tensor y;
+    {
+      Unlocked u;
+      y = at::empty(shape, q.options().dtype(want == GMM_F32 ? at::kFloat : at::kBFloat16));
+      const gmm_tensor qv = view_packed(q), sv = view(scale, code_of(scale.scalar_type())), yv = view(y, (int)want);
+      if (g_entry.widen(x.handle, &qv, &sv, &yv, stream)) x.ok = false;
+    }
+    return x.ok ? give(y) : none();
   });
 }
 

@@ -11,6 +11,7 @@ import ctypes
 import functools
 import importlib.util
 import os
+import warnings
 from typing import Optional
 
 import torch
@@ -35,17 +36,30 @@ EXT_PATH = os.path.join(os.path.dirname(LIB_PATH), "_moe_ext.so")
 _ext = None
 
 
+class _NoExt:
+    """Stands in where _moe_ext.so is not built: every call goes the long way."""
+
+    def set_handle(self, *_):
+        return None
+
+    sort_tokens = dispatch = combine = combine_grad = quant_mxfp4 = widen_mxfp4 = set_handle
+
+
 def _load_ext():
     global _ext
     lib = load()
-    if not os.path.exists(EXT_PATH):
-        raise ImportError(f"{EXT_PATH} is not built; run moe_grouped_matrix_amd.build.build()")
-    spec = importlib.util.spec_from_file_location("_moe_ext", EXT_PATH)
-    ext = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ext)
-    ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
-    for dev, h in _handles.items():
-        ext.set_handle(dev, h)
+    try:
+        spec = importlib.util.spec_from_file_location("_moe_ext", EXT_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+    except ImportError as e:
+        warnings.warn(f"{EXT_PATH} is not built or does not load ({e}); the token and fp4 operators are marshalled in "
+                      "Python, some microseconds a call slower", RuntimeWarning, stacklevel=3)
+        ext = _NoExt()
+    else:
+        ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
+        for dev, h in _handles.items():
+            ext.set_handle(dev, h)
     _ext = ext
     return ext
 

@@ -2,13 +2,16 @@
 _moe_ext.so (host code) beside it with the C++ compiler.
 
 Run ``python -m moe_grouped_matrix_amd.build`` or call ``build()``; the
-libraries are written next to this file."""
+libraries are written next to this file.  libgmm.so needs hipcc alone;
+_moe_ext.so needs a C++ compiler and torch's and Python's headers, and where it
+cannot be built the binding does its work in Python."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -58,6 +61,32 @@ def _run(cmd, verbose):
         raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
 
 
+def _build_ext(tag: str, verbose: bool):
+    """Start compiling _moe_ext.so; returns a function that puts it in place,
+    or takes an old one away and warns."""
+    ext, proc, why = EXT + tag, None, ""
+    try:
+        cmd = _ext_command(ext)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+    except (ImportError, OSError) as e:
+        why = str(e)
+
+    def finish(install: bool) -> None:
+        out, err = proc.communicate() if proc else ("", why)
+        if install and proc and proc.returncode == 0:
+            os.replace(ext, EXT)
+        elif install:
+            # (one of another build may not fit this library)
+            if os.path.exists(EXT):
+                os.remove(EXT)
+            warnings.warn("_moe_ext.so was not built; the token and fp4 operators are marshalled in Python:\n" + out + err)
+        if os.path.exists(ext):
+            os.remove(ext)
+    return finish
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source to an object (in parallel), then link."""
     tag = ".tmp%d" % os.getpid()
@@ -70,25 +99,25 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
         objs.append(obj)
-    ext = EXT + tag
-    cmd = _ext_command(ext)
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    finish_ext = _build_ext(tag, verbose)
     errors = []
     for cmd, pr in procs:
         out, err = pr.communicate()
         if pr.returncode != 0:
             errors.append(" ".join(cmd) + "\n" + out + err)
+    built = False
     try:
         if errors:
-            raise RuntimeError("compiling failed:\n" + "\n".join(errors))
+            raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
         tmp = LIB + tag
         _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
         os.replace(tmp, LIB)
-        os.replace(ext, EXT)
+        built = True
     finally:
-        for o in objs + [ext]:
+        for o in objs:
             if os.path.exists(o):
                 os.remove(o)
+        finish_ext(built)
     return LIB
 
 

@@ -180,7 +180,7 @@ gmm_status run_gmm(gmm_handle* h, const gmm_tensor* lhs, const gmm_tensor* rhs, 
   const int scale_dtype = mx ? GMM_E8M0 : GMM_F32;
   if (rhs_scale) {
     if (rhs_scale->ndim != 4 || rhs_scale->dtype != scale_dtype)
-      return fail(h, GMM_E_INVALID, "expected an f32 (or, with E8M0 scales on both sides, E8M0) 4-tensor for rhs_scale");
+      return fail(h, GMM_E_INVALID, "expected an f32 or E8M0 4-tensor for rhs_scale, of lhs_scale's dtype where both are given");
     nb = rhs_scale->shape[1];
     if (rhs_scale->shape[0] != Ga || rhs_scale->shape[2] != 1 || rhs_scale->shape[3] != N || nb < 1)
       return fail(h, GMM_E_INVALID, "expected rhs_scale of shape (Ga, nb, 1, N), got " + shape_str(rhs_scale));
@@ -497,7 +497,7 @@ gmm_status gmm_device_flags(gmm_handle* h, void* stream, uint32_t* flags) {
       hipMemset(h->flags, 0, sizeof v) != hipSuccess)
     return fail(h, GMM_E_HIP, "reading the device flags failed");
   *flags = v;
-  if (v) return fail(h, GMM_E_DEVICE_DATA, "invalid device-resident group_sizes or group offset (flags " + std::to_string(v) + ")");
+  if (v) return fail(h, GMM_E_DEVICE_DATA, "invalid device-resident group_sizes, group offset or slot_row (flags " + std::to_string(v) + ")");
   return GMM_OK;
 }
 

@@ -20,6 +20,7 @@ namespace gmmh {
 class ErrorTexts {
  public:
   void clear() {
+    if (!any_.load(std::memory_order_relaxed)) return;  // (a thread sees its own set())
     std::lock_guard<std::mutex> lk(mu_);
     const auto it = text_.find(std::this_thread::get_id());
     if (it != text_.end()) it->second.clear();
@@ -27,6 +28,7 @@ class ErrorTexts {
   void set(const std::string& text) {
     std::lock_guard<std::mutex> lk(mu_);
     text_[std::this_thread::get_id()] = text;
+    any_.store(true, std::memory_order_relaxed);
   }
   const char* get() const {
     std::lock_guard<std::mutex> lk(mu_);
@@ -37,6 +39,7 @@ class ErrorTexts {
  private:
   mutable std::mutex mu_;
   std::map<std::thread::id, std::string> text_;
+  std::atomic<bool> any_{false};
 };
 
 }  // namespace gmmh

@@ -31,6 +31,8 @@ namespace {
 // atomics the second launch took 13 us, and so it did read key by key, one key a
 // wave at a time; eight keys a wave at a time 8.9 us; the ids asked for before
 // the counts are waited for, and the scan of the keys in lane shifts, 7.9 us.
+// Reading every workgroup's counts grows with the experts: a call takes 10.6 us
+// at 127 of them, 11.1 at 128, 15.8 at 256 and 41.7 at 1024.
 
 // Inclusive prefix sum and sum over the wave's lanes, by row shifts and row
 // broadcasts (the order of the additions is fixed).
@@ -242,6 +244,11 @@ __global__ __launch_bounds__(T) void sort_place_kernel(SortParams p) {
 // us.  For a decode step of 256 tokens a lane takes one chunk, so that three
 // times the waves share the rows: dispatch 3.7 us (8.7 with a wave a token),
 // combine of f32 rows 4.4 us (13.9).
+//
+// Narrow rows leave lanes idle: 32768 x 8 bf16 rows of 128 columns run at 5.5
+// TB/s (dispatch), 2.6 (combine) and 2.7 (its gradient), of 64 at 3.6, 1.4 and
+// 1.6; from 512 on dispatch and
+// combine run at the copy's rate, the gradient at 0.8 to 1.05 of it.
 
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
@@ -259,7 +266,8 @@ __device__ __forceinline__ Vec<E, V> load_vec(const E* p) {
 #pragma unroll
     for (int i = 0; i < B / 16; ++i) {
       // eight f32 are two loads that share lines, and go without the hint
-      // (combine of 16384 x 8 f32 rows of 1408: 151 against 158 us)
+      // (combine of 16384 x 8 f32 rows of 1408: 152 against 157 us; of bf16 rows
+      // with it 156, without 162)
       if constexpr (B == 32)
         w[i] = reinterpret_cast<const i32x4_any*>(p)[i];
       else
@@ -533,7 +541,11 @@ hipError_t launch_sort(const SortParams& p, int blocks, hipStream_t stream) {
 }
 
 // Chunks a lane takes: a whole row in one segment up to four a lane, but with
-// too few tokens to fill the card one, so that more waves share the rows.
+// too few tokens to fill the card one, so that more waves share the rows.  One /
+// several, us, 8 rows a token, bf16: combine of 1024 tokens x 1408 9.0 / 14.7, of
+// 2048 10.9 / 16.7, of 8192 36.5 / 40.7, of 32768 137 / 156 (several chunks do not
+// pay there either); dispatch within 5% at every size (1024: 5.3 / 5.3, 8192:
+// 36.4 / 38.4, 32768: 152 / 156).
 static int row_unroll(long long tokens, int D, int V, int cu) {
   const int chunks = (D + V - 1) / V;
   const int u = (chunks + 63) / 64;
@@ -542,7 +554,7 @@ static int row_unroll(long long tokens, int D, int V, int cu) {
 }
 
 // Runs launch(p, blocks) over all tokens with `per_token` waves each, in
-// slices of tokens that keep a launch below 2^31 threads.
+// slices of tokens that keep a launch to 2^31 threads at most.
 template <class LaunchFn>
 static hipError_t by_slices(RowParams p, long long per_token, LaunchFn launch) {
   const long long most = (1LL << 25) / per_token > 0 ? (1LL << 25) / per_token : 1;
@@ -605,7 +617,9 @@ static hipError_t grad_u(const RowParams& p, hipStream_t st) {
 
 template <typename G, typename R>
 static hipError_t grad_by_width(RowParams p, int cu, hipStream_t st) {
-  // a wave takes all of a token's slots, or with too few tokens one
+  // a wave takes all of a token's slots, or with too few tokens one (a slot / all,
+  // us, 8 rows of 1408 bf16 a token: 1024 tokens 16.3 / 22.6, 2048 26.6 / 27.8, 2944
+  // 36.8 / 32.7, 8192 92 / 84; rows of 256, 8192 tokens: 32 / 17.5)
   p.part = p.T < 8LL * cu ? 1 : p.k;
   if (p.D < 8) return grad_u<G, R, 1, 1>(p, st);
   switch (((p.D + 7) / 8 + 63) / 64) {

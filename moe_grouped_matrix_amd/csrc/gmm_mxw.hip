@@ -65,7 +65,7 @@ hipError_t launch_big(const Params& p, int cu, int cap, hipStream_t st) {
 hipError_t launch_mxw(const Params& p, SizeClass size, int cu, int cap, hipStream_t st) {
   // The large-group kernel runs a tile in steps of 64, three at least; below
   // that a product is its output's stores, and the few-rows kernel is the
-  // faster one (131072 rows, K = 128, N = 1408: 184 us, 369 MB written).
+  // faster one (131072 rows, K = 128, N = 1408: 181 us, 369 MB written).
   if (size == SizeClass::Big && p.K >= 3 * 64) {
     const bool bias = p.rhs_bias != nullptr;
     if (p.out_f32)

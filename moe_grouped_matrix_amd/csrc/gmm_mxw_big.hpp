@@ -17,14 +17,15 @@
 // and 3 run, so the wait for the next stage and the barrier stand in the
 // middle of a step.
 //
-// 262144 rows x 1408 x 1408, 128 experts: 0.94 ms, 1100 TFLOP/s (the bf16 kernel
-// on widened weights 1.03 ms; a library product of the dense bf16 shape 1.06 ms).
-// The matrix cores are busy 0.62 of the cycles at a clock that the power cap
-// holds near 1.8 GHz; no LDS bank conflicts; without the widening conversions it
-// would take 0.91 ms.  What it saves against the bf16 kernel is operand stream:
-// 43 KB a 64-element step instead of 64.  The few registers that spill are
-// touched at tile boundaries only (they would only lengthen a wait: the constant
-// waits count operations that must at least be there).
+// 262144 rows x 1408 x 1408, 128 experts: 0.94-0.96 ms from card to card, 1086 to
+// 1106 TFLOP/s (the bf16 kernel on widened weights 0.98-1.03 ms; a library product
+// of the dense bf16 shape 1.01-1.06 ms).  The matrix cores are busy 0.62 of the
+// cycles at a clock that the power cap holds near 1.8 GHz; no LDS bank conflicts;
+// without the widening conversions it would take 0.03 ms less.  What it saves
+// against the bf16 kernel is operand stream: 43 KB a 64-element step instead of
+// 64.  The few registers that spill are stored once and read at tile boundaries
+// only (they would only lengthen a wait: the constant waits count operations that
+// must at least be there).
 #pragma once
 
 #include "gmm_big.hpp"

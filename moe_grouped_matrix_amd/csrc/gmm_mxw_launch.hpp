@@ -7,9 +7,17 @@
 namespace gmmk {
 
 // Its size class: the large-group kernel's 256-row tiles pay from about 128
-// rows a group on (32 groups of 128 rows, 1408 x 1408: 29.5 us against 35.0
-// with the few-rows kernel; 128 of 64: 80 against 71; 1 of 4096: 34 against 36;
-// 8 of 256, 4096 x 4096: 104 against 95).
+// rows a group on, and once there are enough of them for the compute units.
+// Few-rows / large-group kernel in us, equal groups:
+//   groups x rows      1408 x 1408    4096 x 4096    N 2048, K 7168
+//   128 x 64            71 / 82       433 / 561      407 / 483
+//   128 x 128          120 / 91       815 / 628      737 / 550
+//   32 x 128            34 / 29       199 / 161      192 / 142
+//   8 x 256             23 / 32        93 / 108       86 / 140
+//   8 x 512             34 / 34       190 / 110      173 / 162
+//   1 x 2048            23 / 31        95 / 81        83 / 123
+//   1 x 4096            33 / 32       178 / 107      148 / 124
+// (One group of 2048 rows of 4096 x 4096 is on its wrong side.)
 inline SizeClass mxw_size(long long M, long long Ga) {
   return M >= 4096 && M >= 128 * Ga ? SizeClass::Big : SizeClass::Small;
 }

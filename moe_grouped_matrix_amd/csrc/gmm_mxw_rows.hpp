@@ -17,8 +17,9 @@
 // while a step is multiplied.  In the result lane (q, r) holds row r and columns
 // 16 q + [0, 16).
 //
-// 2048 rows of 128 experts, 1408 x 1408 (148 MB): 47 us, 3.1 TB/s; 16 rows in
-// every one of 128 groups of 4096 x 4096 (1.1 GB) 4.7 TB/s.  What bounds it: 5 us
+// 2048 rows of 128 experts, 1408 x 1408 (148 MB): 47 us, 3.1 TB/s (39 us with 16
+// rows in every group); 16 rows in every one of 128 groups of 4096 x 4096 (1.17
+// GB) 4.8 TB/s.  What bounds it: 5 us
 // pass before the first weight (launch, group sizes, plan); a bare read of the
 // same weights in the same pieces with a barrier a step takes 29 us; the rest is
 // the lhs, which every column tile reads again through the same L1, and the
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(RowsCfg::T, 2) void gmm_mxw_rows_kernel(Params p) {
   // Every XCD gets a contiguous eighth of the tiles (they share lhs rows and,
   // in groups of more than one row tile, weights in its L2), which its
   // workgroups take in turn.  Whole rounds over the grid left the last round to
-  // some XCDs only: 50 against 40 us for 768 tiles on 512 workgroups.
+  // some XCDs only: 50 against 39 us for 768 tiles on 512 workgroups.
   const int all_items = __builtin_amdgcn_readfirstlane(pl.n_mtiles) * n_ntiles;
   const int X = P % 8 == 0 ? 8 : 1, x = blockIdx.x % X;
   const int step_items = P / X, n_items = (int)((long long)all_items * (x + 1) / X);

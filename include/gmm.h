@@ -32,7 +32,8 @@
  *  - `stream` is a hipStream_t (NULL = the default stream).  gmm_run only
  *    queues work: it never synchronises and never copies group_sizes or the
  *    group offset to the host.
- *  - Several host threads may use a handle at once (gmm_destroy apart).
+ *  - Several host threads may use a handle at once (not gmm_destroy, and not
+ *    gmm_tgmm_run_noalloc, whose calls share memory).
  *  - No exception crosses this boundary.  Every call returns a gmm_status;
  *    gmm_last_error() gives the text of the calling thread's last failure on
  *    a handle.

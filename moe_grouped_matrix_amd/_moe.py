@@ -11,6 +11,7 @@ import ctypes
 import functools
 import importlib.util
 import os
+import threading
 import warnings
 from typing import Optional
 
@@ -34,6 +35,7 @@ _PACKED_DTYPE = {torch.uint8: GMM_F4E2M1, torch.float4_e2m1fn_x2: GMM_F4E2M1}
 # then goes the long way below and is told why.
 EXT_PATH = os.path.join(os.path.dirname(LIB_PATH), "_moe_ext.so")
 _ext = None
+_ext_lock = threading.Lock()
 
 
 class _NoExt:
@@ -48,20 +50,23 @@ class _NoExt:
 def _load_ext():
     global _ext
     lib = load()
-    try:
-        spec = importlib.util.spec_from_file_location("_moe_ext", EXT_PATH)
-        ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(ext)
-    except ImportError as e:
-        warnings.warn(f"{EXT_PATH} is not built or does not load ({e}); the token and fp4 operators are marshalled in "
-                      "Python, some microseconds a call slower", RuntimeWarning, stacklevel=3)
-        ext = _NoExt()
-    else:
-        ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
-        for dev, h in _handles.items():
-            ext.set_handle(dev, h)
-    _ext = ext
-    return ext
+    with _ext_lock:
+        if _ext is not None:
+            return _ext
+        try:
+            spec = importlib.util.spec_from_file_location("_moe_ext", EXT_PATH)
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+        except ImportError as e:
+            warnings.warn(f"{EXT_PATH} is not built or does not load ({e}); the token and fp4 operators are marshalled "
+                          "in Python, some microseconds a call slower", RuntimeWarning, stacklevel=3)
+            ext = _NoExt()
+        else:
+            ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
+            for dev, h in list(_handles.items()):
+                ext.set_handle(dev, h)
+        _ext = ext
+        return ext
 
 
 def _current(t) -> int:

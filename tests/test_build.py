@@ -82,3 +82,24 @@ def test_operators_run_without_the_extension(tmp_path, monkeypatch, there):
     assert _moe.dispatch(x, slots, out=out, stream=Stream(3)) is out  # (no second warning: those are errors here)
     assert ran == ["gmm_dispatch_run"] * 2
 
+
+
+def test_threads_load_one_extension(monkeypatch):
+    """A second load would forget the handles that the first one was given."""
+    import threading
+    if not os.path.exists(_moe.EXT_PATH):
+        build.build()
+    monkeypatch.setattr(_moe, "_ext", None)
+    real, loads = _moe.importlib.util.module_from_spec, []
+    monkeypatch.setattr(_moe.importlib.util, "module_from_spec", lambda spec: loads.append(spec) or real(spec))
+    barrier, got = threading.Barrier(8), []
+
+    def run():
+        barrier.wait()
+        got.append(_moe._load_ext())
+    threads = [threading.Thread(target=run) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(loads) == 1 and len(got) == 8 and all(e is got[0] for e in got)

@@ -125,6 +125,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gmm_quant_mxfp4_run.restype = ctypes.c_int
             lib.gmm_widen_mxfp4_run.argtypes = [vp, vp, vp, vp, vp]
             lib.gmm_widen_mxfp4_run.restype = ctypes.c_int
+            # and so do these (_layer.py)
+            f32, i = ctypes.c_float, ctypes.c_int
+            lib.gmm_route_run.argtypes = [vp, vp, vp, vp, i, i, f32, vp, vp, vp]
+            lib.gmm_route_run.restype = i
+            lib.gmm_balance_loss_workspace.argtypes = [i64, i64, ctypes.POINTER(sz)]
+            lib.gmm_balance_loss_workspace.restype = i
+            lib.gmm_balance_loss_run.argtypes = [vp, vp, vp, vp, i, f32, f32, vp, vp, vp, vp, sz, vp]
+            lib.gmm_balance_loss_run.restype = i
+            lib.gmm_router_grad_run.argtypes = [vp, vp, vp, vp, i, vp, i, f32, vp, vp, vp, f32, f32, vp, vp]
+            lib.gmm_router_grad_run.restype = i
+            lib.gmm_gmv_workspace.argtypes = [i64, i64, i, ctypes.POINTER(sz)]
+            lib.gmm_gmv_workspace.restype = i
+            lib.gmm_gmv_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            lib.gmm_gmv_run.restype = i
+            lib.gmm_adamw_run.argtypes = [vp, vp, i64, vp, vp]
+            lib.gmm_adamw_run.restype = i
             _lib = lib
     return _lib
 

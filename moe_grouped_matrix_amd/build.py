@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libgmm.so")
 EXT = os.path.join(HERE, "_moe_ext.so")  # the Python side of gmm_moe.h (host code over torch's C++ API)
 SOURCES = [os.path.join(CSRC, n) for n in
            ("gmm_kernels.hip", "gmm_w8a8.hip", "gmm_stream.hip", "gmm_quant.hip", "gmm_moe.hip", "gmm_mxfp4.hip", "gmm_mxw.hip",
-            "gmm_api.cpp", "gmm_moe_api.cpp")]
+            "gmm_router.hip", "gmm_gmv.hip", "gmm_adamw.hip", "gmm_api.cpp", "gmm_moe_api.cpp", "gmm_layer_api.cpp")]
 
 # Packed fp32 VALU instructions are kept out of the generated code.
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -9,8 +9,8 @@ from ._binding import (EXPORTED, FLAG_BAD_OFFSET, FLAG_NEGATIVE_SIZE, FLAG_SCHED
                        LIB_PATH, GmmDeviceDataError, GmmError, GmmInvalid, GmmUnsupported,
                        debug_worklist, device_flags, gmm, handle, load, quant_fp8, set_grid_limit,
                        set_tile_policy, tgmm, widen_scales)
-from ._layer import ADAMW_BLOCK, EXPORTED_LAYER, adamw, balance_loss, gmv, route, router_grad  # noqa: F401
-from ._moe import (EXPORTED_MOE, FLAG_BAD_ROW, combine, combine_grad, dispatch, quant_mxfp4,  # noqa: F401
+from ._layer import ADAMW_BLOCK, adamw, balance_loss, gmv, route, router_grad  # noqa: F401
+from ._moe import (EXPORTED_LAYER, EXPORTED_MOE, FLAG_BAD_ROW, combine, combine_grad, dispatch, quant_mxfp4,  # noqa: F401
                    sort_tokens, widen_mxfp4)
 
 __all__ = ["gmm", "tgmm", "quant_fp8", "widen_scales", "sort_tokens", "dispatch", "combine", "combine_grad",

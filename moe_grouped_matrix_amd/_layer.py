@@ -3,7 +3,8 @@ mixture-of-experts layer with its balance loss and their gradient, the experts'
 products of a few tokens by expert id, and the AdamW step.
 
 Argument marshalling only, as in _binding.py and _moe.py: the checks of values
-and the computation are the library's."""
+and the computation are the library's, and the common call is marshalled by
+_moe_ext.so."""
 from __future__ import annotations
 
 import ctypes
@@ -14,10 +15,9 @@ from typing import Optional, Sequence, Tuple, Union
 import torch
 
 from ._binding import _DTYPE, _empty, GMM_BF16, GMM_F32, GMM_F8E4M3FN, GmmTensor, load, PACKED_FORMATS
-from ._moe import _ID_DTYPE, _PACKED_DTYPE, _device, _out, _pack, _refuse, _run
+from . import _moe
+from ._moe import _current, _device, _ID_DTYPE, _load_ext, _out, _pack, _PACKED_DTYPE, _refuse, _run
 
-EXPORTED_LAYER = ("gmm_route_run", "gmm_balance_loss_workspace", "gmm_balance_loss_run", "gmm_router_grad_run",
-                  "gmm_gmv_workspace", "gmm_gmv_run", "gmm_adamw_run")
 ADAMW_BLOCK = 256
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -50,8 +50,12 @@ def route(logits: torch.Tensor, top_k: int, *, scores: str = "softmax", bias: Op
     is never chosen; choices that are missing, and all of a token whose valid
     [T] (bool) is False, are id -1 with weight 0.  The gradient is
     router_grad()."""
+    kind, k = _kind(scores), int(top_k)
+    if expert_ids is None and weights is None and stream is None:
+        made = (_moe._ext or _load_ext()).route(logits, k, bias, valid, kind, bool(renormalize), scale, _current(logits))
+        if made is not None:
+            return made
     dev = _device(logits, "logits")
-    k = int(top_k)
     T = logits.shape[0] if logits.dim() == 2 else 0
     args = [_pack(logits, "logits", dev), _maybe(bias, "bias", dev), _maybe(valid, "valid", dev, _VALID_DTYPE)]
     # (a number of choices that is out of range is refused by the run, whatever the output holds)
@@ -59,7 +63,7 @@ def route(logits: torch.Tensor, top_k: int, *, scores: str = "softmax", bias: Op
     if expert_ids.dim() != 2 or expert_ids.shape[1] != k:
         _refuse("expert_ids must hold top_k choices a token")
     weights, wv = _out(weights, "weights", (T, min(max(k, 0), 1025)), torch.float32, dev, stream)
-    _run(load().gmm_route_run, dev, stream, (logits, bias, valid, expert_ids, weights), *args, _kind(scores),
+    _run(load().gmm_route_run, dev, stream, (logits, bias, valid, expert_ids, weights), *args, kind,
          int(bool(renormalize)), float(scale), iv, wv)
     return expert_ids, weights
 
@@ -86,6 +90,11 @@ def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, *, scores: str 
     whose valid [T] (bool) is False, or whose logits are all -inf, count for
     nothing; tokens is the number of the others.  The gradient is
     router_grad(), which takes the counts and tokens."""
+    kind = _kind(scores)
+    if loss is None and counts is None and tokens is None and stream is None:
+        made = (_moe._ext or _load_ext()).balance_loss(logits, expert_ids, valid, kind, coef, z_coef, _current(logits))
+        if made is not None:
+            return made
     dev = _device(logits, "logits")
     T, E = logits.shape if logits.dim() == 2 else (0, 1)
     args = [_pack(logits, "logits", dev), _pack(expert_ids, "expert_ids", dev, _ID_DTYPE),
@@ -95,7 +104,7 @@ def balance_loss(logits: torch.Tensor, expert_ids: torch.Tensor, *, scores: str 
     tokens, tv = _out(tokens, "tokens", (1,), torch.int32, dev, stream)
     need = _balance_workspace(T, E)
     work = _empty((need,), torch.uint8, dev, stream) if need else None
-    _run(load().gmm_balance_loss_run, dev, stream, (logits, expert_ids, valid, loss, counts, tokens), *args, _kind(scores),
+    _run(load().gmm_balance_loss_run, dev, stream, (logits, expert_ids, valid, loss, counts, tokens), *args, kind,
          float(coef), float(z_coef), lv, cv, tv, work.data_ptr() if need else None, need)
     return loss, counts, tokens
 
@@ -114,6 +123,12 @@ def router_grad(logits: torch.Tensor, expert_ids: torch.Tensor, *, dweights: Opt
     forward calls; the counts are constants, and may be sums over ranks.
     Returns dlogits [T,E] of logits' dtype, zeros for tokens that count for
     nothing and for experts that are switched off."""
+    kind = _kind(scores)
+    if dlogits is None and stream is None:
+        made = (_moe._ext or _load_ext()).router_grad(logits, expert_ids, valid, kind, dweights, bool(renormalize), scale, counts,
+                                                      tokens, dloss, coef, z_coef, _current(logits))
+        if made is not None:
+            return made
     dev = _device(logits, "logits")
     args = [_pack(logits, "logits", dev), _pack(expert_ids, "expert_ids", dev, _ID_DTYPE),
             _maybe(valid, "valid", dev, _VALID_DTYPE)]
@@ -121,7 +136,7 @@ def router_grad(logits: torch.Tensor, expert_ids: torch.Tensor, *, dweights: Opt
     wv = _maybe(dweights, "dweights", dev)
     dlogits, dv = _out(dlogits, "dlogits", logits.shape, logits.dtype, dev, stream)
     _run(load().gmm_router_grad_run, dev, stream, (logits, expert_ids, valid, dweights, counts, tokens, dloss, dlogits), *args,
-         _kind(scores), wv, int(bool(renormalize)), float(scale), *more, float(coef), float(z_coef), dv)
+         kind, wv, int(bool(renormalize)), float(scale), *more, float(coef), float(z_coef), dv)
     return dlogits
 
 
@@ -157,6 +172,11 @@ def gmv(x: torch.Tensor, rhs: torch.Tensor, expert_ids: Optional[torch.Tensor] =
     [0,G) giving zeros (None with one group: a dense product).  Returns
     [T,k,N] of out_dtype, or with weights [T,k] the weighted sum over a token's
     slots, [T,N].  Up to 4096 slots; more rows belong to gmm()."""
+    if out is None and stream is None:
+        made = (_moe._ext or _load_ext()).gmv(x, rhs, PACKED_FORMATS.get(rhs_format, -1), rhs_scale, rhs_zero, expert_ids, weights,
+                                              _DTYPE.get(out_dtype, -2), _current(x))
+        if made is not None:
+            return made
     dev = _device(x, "x")
     N = rhs.shape[1] if rhs.dim() == 3 else 1
     T = x.shape[0] if x.dim() else 0
@@ -229,6 +249,10 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg
 
     The products' weights are parameters like any other: params [G,K,N], grads
     as tgmm() returns them."""
+    if stream is None and len(params):
+        if (_moe._ext or _load_ext()).adamw(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, step, lr,
+                                            *betas, eps, weight_decay, grad_scale, _current(params[0])):
+            return
     if len(params) == 0:
         load()
         if any(len(t) for t in (grads, exp_avg, exp_avg_sq, exp_avg_scale or (), exp_avg_sq_scale or (), copies or ())):

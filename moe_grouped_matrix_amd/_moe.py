@@ -20,9 +20,11 @@ import torch
 from ._binding import (_DTYPE, _PAD, _TENSOR, _empty, _handles, _raise, _raw_stream, _record, GMM_E_INVALID,
                        GMM_F4E2M1, GMM_I64, GmmInvalid, LIB_PATH, handle, load)
 
-# in the order of _moe_ext's bind()
+# in the order of _moe_ext's bind() and bind_layer()
 EXPORTED_MOE = ("gmm_sort_tokens_workspace", "gmm_sort_tokens_run", "gmm_dispatch_run", "gmm_combine_run",
                 "gmm_combine_grad_run", "gmm_quant_mxfp4_run", "gmm_widen_mxfp4_run")
+EXPORTED_LAYER = ("gmm_route_run", "gmm_balance_loss_workspace", "gmm_balance_loss_run", "gmm_router_grad_run",
+                  "gmm_gmv_workspace", "gmm_gmv_run", "gmm_adamw_run")
 FLAG_BAD_ROW = 0x10
 
 _ID_DTYPE = {torch.int32: _DTYPE[torch.int32], torch.int64: GMM_I64}
@@ -45,6 +47,7 @@ class _NoExt:
         return None
 
     sort_tokens = dispatch = combine = combine_grad = quant_mxfp4 = widen_mxfp4 = set_handle
+    route = balance_loss = router_grad = gmv = adamw = set_handle
 
 
 def _load_ext():
@@ -62,7 +65,8 @@ def _load_ext():
                           "in Python, some microseconds a call slower", RuntimeWarning, stacklevel=3)
             ext = _NoExt()
         else:
-            ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED_MOE])
+            for bind, names in ((ext.bind, EXPORTED_MOE), (ext.bind_layer, EXPORTED_LAYER)):
+                bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names])
             for dev, h in list(_handles.items()):
                 ext.set_handle(dev, h)
         _ext = ext

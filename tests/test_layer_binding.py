@@ -5,14 +5,26 @@ by Python objects that keep account)."""
 import pytest
 import torch
 
-from moe_grouped_matrix_amd import _binding, _layer
+from moe_grouped_matrix_amd import _binding, _layer, _moe
 from test_stream_argument import _empty, Stream, check, device, kept, streams  # noqa: F401  (a fixture)
 
 F32, BF16, I32, I64, U8, E4 = (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float8_e4m3fn)
 
 
+class Ext:
+    """Takes no call: every one is marshalled in Python."""
+
+    def __getattr__(self, name):
+        return lambda *_: None
+
+
 @pytest.fixture(autouse=True)
-def clear():
+def clear(monkeypatch, request):
+    if "streams" in request.fixturenames:
+        request.getfixturevalue("streams")
+        monkeypatch.setattr(_moe, "_ext", Ext())
+        monkeypatch.setattr(_moe, "_current", lambda t: 0)
+        monkeypatch.setattr(_layer, "_current", lambda t: 0)
     for cached in (_layer._balance_workspace, _layer._gmv_workspace):
         cached.cache_clear()
     yield

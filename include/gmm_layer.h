@@ -86,7 +86,7 @@ gmm_status gmm_route_run(gmm_handle* h,
 
 /*
  * gmm_balance_loss_workspace: bytes of workspace that gmm_balance_loss_run
- * needs for T tokens and E experts.
+ * needs for T tokens and E experts (0 for a few tokens).
  */
 gmm_status gmm_balance_loss_workspace(int64_t tokens, int64_t experts, size_t* bytes);
 

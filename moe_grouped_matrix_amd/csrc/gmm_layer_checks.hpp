@@ -50,16 +50,17 @@ inline Check check_route(const gmm_tensor* logits, const gmm_tensor* bias, const
   return check_memory({logits, bias, valid}, {ids, weights});
 }
 
-// Workgroups of the balance loss's first launch: one workgroup alone would
-// need no second launch, but the counting launch of few tokens costs little.
+// Workgroups of the balance loss's first launch, 64 tokens (16 of more than
+// 128 experts) at a time.  One workgroup alone needs no second launch and no
+// workspace.
 inline int balance_blocks(long long T, long long E) {
-  const long long rows = E <= 128 ? 16 : 4;  // tokens that a workgroup takes at once
-  long long b = (T + rows - 1) / rows;
-  b = b > 256 ? 256 : b;
-  return (int)(b < 1 ? 1 : b);
+  const long long rows = E <= 128 ? 64 : 16;
+  const long long b = (T + rows - 1) / rows;
+  return (int)(b < 1 ? 1 : b > 256 ? 256 : b);
 }
 inline size_t balance_workspace_bytes(long long T, long long E) {
-  return (size_t)balance_blocks(T, E) * (size_t)(2 * E + 2) * sizeof(float);
+  const int blocks = balance_blocks(T, E);
+  return blocks == 1 ? 0 : (size_t)blocks * (size_t)(2 * E + 2) * sizeof(float);
 }
 
 inline Check check_workspace(const void* workspace, size_t bytes, size_t need,

@@ -9,7 +9,8 @@
 
 namespace gmmk {
 
-constexpr int kRouterT = 256;  // threads of the router kernels: four waves
+constexpr int kRouterT = 256;    // threads of the choice and the gradient: four waves
+constexpr int kBalanceT = 1024;  // of the balance loss: a thread an expert at its end
 
 // The router's tensors: T tokens, E experts, k choices.
 struct RouterParams {
@@ -27,7 +28,7 @@ struct RouterParams {
   float* loss_out;        // [1]
   int32_t* counts_out;    // [E]
   int32_t* tokens_out;    // [1]
-  float* work;            // balance loss: [blocks][2 E + 2]
+  float* work;            // balance loss: blocks * (2 E + 2) words
   long long T;
   int32_t E, k;
   int32_t x_f32, ids64, dw_f32, sigmoid, renorm;

@@ -3,8 +3,8 @@
 // counts, and the gradient of both.  Layouts and meanings are those of
 // gmm_layer.h.
 //
-// All three kernels give a token a group of L lanes (a DPP row of 16 or the
-// whole wave), lane l of which holds experts l + L v, so that a group's loads
+// All three kernels give a token a group of L lanes (half a DPP row, a row, or
+// the whole wave), lane l of which holds experts l + L v, so that a group's loads
 // are coalesced whatever E's alignment is and a token's sums and maxima stay
 // in registers.  Everything is fp32.
 #include <hip/hip_runtime.h>
@@ -22,7 +22,7 @@ constexpr float kNan = __builtin_nanf("");
 
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);  // (every lane reads another)
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -42,7 +42,7 @@ __device__ __forceinline__ T reduce(T v, Op op) {
   v = op(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
   v = op(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
   v = op(v, dpp<0x141>(v));  // row_half_mirror
-  v = op(v, dpp<0x140>(v));  // row_mirror
+  if constexpr (L >= 16) v = op(v, dpp<0x140>(v));  // row_mirror
   if constexpr (L == 64) {
     v = op(v, __shfl_xor(v, 16, 64));
     v = op(v, __shfl_xor(v, 32, 64));
@@ -65,14 +65,42 @@ template <int L>
 __device__ __forceinline__ bool group_any(bool b) {
   const unsigned long long m = __ballot(b);
   if constexpr (L == 64) return m != 0;
-  return ((m >> (threadIdx.x & 48)) & 0xFFFF) != 0;
+  return ((m >> (threadIdx.x & 63 & ~(L - 1))) & ((1ull << (L & 63)) - 1)) != 0;
 }
 
 __device__ __forceinline__ float load_value(const void* p, long long i, bool f32) {
   return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// e^x of an x that is at most 0 (or -inf), within 2 u of itself: 2^t by the
+// exponential instruction (1 ulp), t = x log2 e rounded, times 1 + (what the
+// rounding left) ln 2.  Below 2^-126 it gives 0.
+__device__ __forceinline__ float exp_of(float x) {
+  x = fmaxf(x, -160.f);  // (2^-230: 0; no infinity meets the fma)
+  const float t = x * 0x1.715476p+0f;
+  const float left = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, left * 0x1.62e43p-1f, e);
+}
+
+// The sigmoids of z and of -z, each within a few u of itself.
+__device__ __forceinline__ void sigmoids(float z, float& s, float& not_s) {
+  const float e = exp_of(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
+  s = z >= 0.f ? r : er;
+  not_s = z >= 0.f ? er : r;
+}
+__device__ __forceinline__ float sigmoid(float z) {
+  float s, n;
+  sigmoids(z, s, n);
+  return s;
+}
+
+// Choice j of token t, -1 where there is none.
+__device__ __forceinline__ long long load_id(const RouterParams& p, long long t, int j) {
+  if (t >= p.T || j >= p.k) return -1;
+  const long long i = t * p.k + j;
+  return p.ids64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
+}
 
 // A token's logits over its lanes (-inf where there is no expert).
 template <int V>
@@ -83,23 +111,38 @@ struct Row {
   bool bad;     // counts, and holds a NaN or +inf
 };
 
+// Asks for the logits; what is out of range is read elsewhere in the tensor
+// (which must have a token) and put right by row_state, so that the loads need
+// no branches.
 template <int L, int V>
-__device__ __forceinline__ Row<V> load_row(const RouterParams& p, long long t, int l) {
-  Row<V> r;
-  const bool valid = t < p.T && (!p.valid || p.valid[t] != 0);
+__device__ __forceinline__ bool load_row(Row<V>& r, const RouterParams& p, long long t, int l) {
+  const long long row = (t < p.T ? t : p.T - 1) * p.E;
+  const int last = p.E - 1;
+  if (p.x_f32) {
+    const float* const z = static_cast<const float*>(p.logits) + row;
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.z[v] = z[l + L * v < last ? l + L * v : last];
+  } else {
+    const uint16_t* const z = static_cast<const uint16_t*>(p.logits) + row;
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.z[v] = bf16_bits_to_f32(z[l + L * v < last ? l + L * v : last]);
+  }
+  return t < p.T && (!p.valid || p.valid[t] != 0);
+}
+
+template <int L, int V>
+__device__ __forceinline__ void row_state(Row<V>& r, const RouterParams& p, bool valid, int l) {
   float top = -kInf;
   bool bad = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = l + L * v;
-    r.z[v] = valid && e < p.E ? load_value(p.logits, t * p.E + e, p.x_f32) : -kInf;
+    r.z[v] = valid && l + L * v < p.E ? r.z[v] : -kInf;
     top = fmaxf(top, r.z[v]);
     bad |= !(r.z[v] < kInf);
   }
   r.top = group_max<L>(top);
   r.bad = group_any<L>(bad);
   r.counts = r.bad || r.top > -kInf;
-  return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -107,6 +150,12 @@ __device__ __forceinline__ Row<V> load_row(const RouterParams& p, long long t, i
 // its low 29 bits zero, and ten of them take the id, so that of equal values
 // the lower id is the larger key (for negative values larger bits are smaller
 // keys), every key is another, and one maximum finds both.
+//
+// Up to eight choices (K8), a lane first brings its values into order, eight at
+// a time by a network of 19 exchanges (a maximum and a minimum each), lists of
+// eight being merged to their eight largest; a round then looks at the heads of
+// the lanes' lists alone, and the lane that held the best one moves its list
+// up.  More choices, and few values a lane, look at every value in every round.
 
 __device__ __forceinline__ double choice_key(float value, int e) {
   const float x = value + 0.f;  // (-0 ranks as +0)
@@ -119,54 +168,120 @@ __device__ __forceinline__ int key_expert(double key) {
   return key < 0 ? tag : 1023 - tag;
 }
 
-template <int L, int V>
-__global__ __launch_bounds__(kRouterT) void route_kernel(RouterParams p) {
+__device__ __forceinline__ void exchange(double& a, double& b) {  // the larger first
+  const double hi = __builtin_fmax(a, b);
+  b = __builtin_fmin(a, b);
+  a = hi;
+}
+// A bitonic list of eight into falling order.
+__device__ __forceinline__ void order_bitonic(double* k) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) exchange(k[i], k[i + d]);
+}
+// Eight keys into falling order (Batcher's odd-even merge sort).
+__device__ __forceinline__ void order8(double* k) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) exchange(k[i], k[i + 1]);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    exchange(k[i], k[i + 2]);
+    exchange(k[i + 1], k[i + 3]);
+    exchange(k[i + 1], k[i + 2]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) exchange(k[i], k[i + 4]);
+  exchange(k[2], k[4]);
+  exchange(k[3], k[5]);
+  exchange(k[1], k[2]);
+  exchange(k[3], k[4]);
+  exchange(k[5], k[6]);
+}
+
+template <int L, int V, bool K8>
+__global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
   constexpr int R = 64 / L;
   const int l = threadIdx.x & (L - 1), r = (threadIdx.x & 63) / L, w = threadIdx.x >> 6;
   constexpr int W = kRouterT / 64;
   for (long long t0 = (long long)blockIdx.x * (W * R); t0 < p.T; t0 += (long long)gridDim.x * (W * R)) {
     const long long t = t0 + w * R + r;
-    Row<V> x = load_row<L, V>(p, t, l);
-    float sum = 0.f;  // of the softmax, relative to the largest logit
+    Row<V> x;
+    const bool valid = load_row<L, V>(x, p, t, l);
+    row_state<L, V>(x, p, valid, l);
+    float over_sum = 0.f;  // of the softmax, relative to the largest logit
     if (!p.sigmoid && (p.bias || !p.renorm)) {
+      float sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum += x.counts ? expf(x.z[v] - x.top) : 0.f;
-      sum = group_sum<L>(sum);
+      for (int v = 0; v < V; ++v) sum += exp_of(x.z[v] - x.top);
+      over_sum = 1.f / group_sum<L>(sum);
     }
     double key[V];
     bool bad = x.bad;
+    if (p.bias) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = l + L * v;
-      float rank = x.z[v];
-      if (p.bias && rank > -kInf && e < p.E) {
-        rank = (p.sigmoid ? sigmoid(rank) : expf(rank - x.top) / sum) + p.bias[e];
-        bad |= !(rank < kInf);
+      for (int v = 0; v < V; ++v) {
+        const int e = l + L * v;
+        float rank = x.z[v];
+        if (rank > -kInf && e < p.E) {
+          rank = (p.sigmoid ? sigmoid(rank) : exp_of(rank - x.top) * over_sum) + p.bias[e];
+          bad |= !(rank < kInf);
+        }
+        key[v] = choice_key(rank, e);
       }
-      key[v] = choice_key(rank, e);
+      bad = group_any<L>(bad);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = choice_key(x.z[v], l + L * v);
     }
-    if (p.bias) bad = group_any<L>(bad);
-    // round by round; lane j keeps the j-th choice
+    // lane j keeps the j-th choice
     double mine = -__builtin_inf();
-    for (int j = 0; j < p.k; ++j) {
-      double best = key[0];
+    if constexpr (K8) {
 #pragma unroll
-      for (int v = 1; v < V; ++v) best = __builtin_fmax(best, key[v]);
-      best = group_max<L>(best);
+      for (int i = 0; i < V; i += 8) order8(key + i);
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = key[v] == best ? -__builtin_inf() : key[v];
-      if (l == j) mine = best;
+      for (int n = V / 8; n > 1; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) key[8 * i + j] = __builtin_fmax(key[8 * i + j], key[8 * (i + n / 2) + 7 - j]);
+          order_bitonic(key + 8 * i);
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j == p.k) break;
+        const double best = group_max<L>(key[0]);
+        mine = l == j ? best : mine;
+        const bool won = key[0] == best;
+#pragma unroll
+        for (int i = 0; i < 7 - j; ++i) key[i] = won ? key[i + 1] : key[i];
+      }
+    } else {
+      for (int j = 0; j < p.k; ++j) {
+        double best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = __builtin_fmax(best, key[v]);
+        best = group_max<L>(best);
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? -__builtin_inf() : key[v];
+        mine = l == j ? best : mine;
+      }
     }
     const bool there = mine > -__builtin_inf() && !bad;
     const int id = there ? key_expert(mine) : -1;
-    float s = 0.f;
-    if (there) s = load_value(p.logits, t * p.E + id, p.x_f32);
+    float z = -kInf;
+    if (!p.bias)
+      z = there ? (float)__longlong_as_double(__double_as_longlong(mine) & ~1023ll) : -kInf;
+    else if (there)
+      z = load_value(p.logits, t * p.E + id, p.x_f32);
+    float s;
     if (p.sigmoid) {
-      s = there ? sigmoid(s) : 0.f;
+      s = there ? sigmoid(z) : 0.f;
     } else {
-      const float from = p.renorm ? group_max<L>(there ? s : -kInf) : x.top;
-      s = there ? expf(s - from) : 0.f;
-      if (!p.renorm) s = s / sum;
+      const float from = p.renorm ? group_max<L>(z) : x.top;
+      s = there ? exp_of(z - from) : 0.f;
+      if (!p.renorm) s *= over_sum;
     }
     if (p.renorm) {
       const float total = group_sum<L>(s);
@@ -181,122 +296,189 @@ __global__ __launch_bounds__(kRouterT) void route_kernel(RouterParams p) {
 
 // ---------------------------------------------------------------------------
 // The balance loss: every workgroup's sums of p, counts of choices, sum of
-// squared logsumexp and count of tokens, in a row of the workspace; a second
-// launch adds the rows up in order.
+// squared logsumexp and count of tokens, in the workspace (planes [blocks][E]
+// of sums and of counts, then [blocks] of each of the others); a second launch
+// adds them up in order.  One workgroup alone finishes by itself.
+
+// loss, given thread e's sum of p and count of expert e (0 past the last).
+__device__ __forceinline__ void finish_loss(const RouterParams& p, double P, long long count, double z2, int tokens) {
+  __shared__ double dots[kBalanceT / 64], alls[kBalanceT / 64];
+  double dot = (double)count * P, all = (double)count;
+  dot = group_sum<64>(dot);
+  all = group_sum<64>(all);
+  if ((threadIdx.x & 63) == 0) {
+    dots[threadIdx.x >> 6] = dot;
+    alls[threadIdx.x >> 6] = all;
+  }
+  if ((int)threadIdx.x < p.E) p.counts_out[threadIdx.x] = (int)count;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    dot = all = 0;
+    for (int i = 0; i < kBalanceT / 64; ++i) {
+      dot += dots[i];
+      all += alls[i];
+    }
+    const double n = tokens > 0 ? tokens : 1;
+    p.loss_out[0] = (float)((double)p.coef * p.E * dot / ((all > 0 ? all : 1) * n) + (double)p.z_coef * z2 / n);
+    p.tokens_out[0] = tokens;
+  }
+}
 
 template <int L, int V>
-__global__ __launch_bounds__(kRouterT) void balance_partial_kernel(RouterParams p) {
-  constexpr int R = 64 / L, W = kRouterT / 64;
+__global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams p) {
+  constexpr int R = 64 / L, W = kBalanceT / 64;
   __shared__ int hist[kMaxGroups];
-  __shared__ float part[W * R][L * V];
-  __shared__ float zsum[W * R];
-  __shared__ int nsum[W * R];
+  __shared__ float part[W][L * V];
+  __shared__ float zsum[W];
+  __shared__ int nsum[W];
   const int l = threadIdx.x & (L - 1), r = (threadIdx.x & 63) / L, w = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < p.E; e += kRouterT) hist[e] = 0;
+  if ((int)threadIdx.x < p.E) hist[threadIdx.x] = 0;
   __syncthreads();
   float acc[V], z2 = 0.f;
   int n = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (long long t0 = (long long)blockIdx.x * (W * R); t0 < p.T; t0 += (long long)gridDim.x * (W * R)) {
-    const long long t = t0 + w * R + r;
-    Row<V> x = load_row<L, V>(p, t, l);
-    float e[V], sum = 0.f, ssum = 0.f;
+  // the next token is asked for before the present one is worked on
+  const long long step = (long long)gridDim.x * (W * R);
+  long long t = (long long)blockIdx.x * (W * R) + w * R + r;
+  const long long end = p.T + w * R + r;
+  Row<V> next;
+  bool next_valid = false;
+  if (p.T > 0) next_valid = load_row<L, V>(next, p, t, l);  // (there may be no token at all)
+  long long id = load_id(p, t, l);
+  for (; t < end; t += step) {
+    Row<V> x = next;
+    const bool valid = next_valid;
+    if (t + step < end) next_valid = load_row<L, V>(next, p, t + step, l);
+    if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+    for (int j = l + L; j < p.k; j += L) {
+      id = load_id(p, t, j);
+      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+    }
+    id = load_id(p, t + step, l);
+    row_state<L, V>(x, p, valid, l);
+    float e[V], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      e[v] = x.counts ? expf(x.z[v] - x.top) : 0.f;
+      e[v] = exp_of(x.z[v] - x.top);
       sum += e[v];
     }
     sum = group_sum<L>(sum);
     const float lse = x.bad ? kNan : x.top + logf(sum);
     if (p.sigmoid) {
+      sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        e[v] = x.counts && x.z[v] > -kInf ? sigmoid(x.z[v]) : 0.f;
-        ssum += e[v];
+        e[v] = x.z[v] > -kInf ? sigmoid(x.z[v]) : 0.f;
+        sum += e[v];
       }
-      sum = group_sum<L>(ssum);
+      sum = group_sum<L>(sum);
     }
     if (x.counts) {
+      const float over = x.bad ? kNan : sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += x.bad ? kNan : sum > 0.f ? e[v] / sum : 0.f;
-      z2 += lse * lse;
+      for (int v = 0; v < V; ++v) acc[v] = __builtin_fmaf(e[v], over, acc[v]);
+      z2 = __builtin_fmaf(lse, lse, z2);
       ++n;
     }
-    if (t < p.T)
-      for (int j = l; j < p.k; j += L) {
-        const long long i = t * p.k + j;
-        const long long id = p.ids64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
-        if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-      }
   }
+  // the wave's groups (they hold the same experts), then the workgroup's waves
 #pragma unroll
-  for (int v = 0; v < V; ++v) part[w * R + r][l + L * v] = acc[v];
-  if (l == 0) {
-    zsum[w * R + r] = z2;
-    nsum[w * R + r] = n;
+  for (int s = L; s < 64; s *= 2) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] += __shfl_xor(acc[v], s, 64);
+    z2 += __shfl_xor(z2, s, 64);
+    n += __shfl_xor(n, s, 64);
+  }
+  if (r == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[w][l + L * v] = acc[v];
+  }
+  if ((threadIdx.x & 63) == 0) {
+    zsum[w] = z2;
+    nsum[w] = n;
   }
   __syncthreads();
-  float* const out = p.work + (long long)blockIdx.x * (2 * p.E + 2);
-  for (int e = threadIdx.x; e < p.E; e += kRouterT) {
-    float s = 0.f;
+  const int e = threadIdx.x, B = gridDim.x, b = blockIdx.x;
+  float P = 0.f, z = 0.f;
+  int c = 0;
+  if (e < p.E)
 #pragma unroll
-    for (int i = 0; i < W * R; ++i) s += part[i][e];
-    out[e] = s;
-    reinterpret_cast<int*>(out)[p.E + e] = hist[e];
+    for (int i = 0; i < W; ++i) P += part[i][e];
+  for (int i = 0; i < W; ++i) {
+    z += zsum[i];
+    c += nsum[i];
   }
-  if (threadIdx.x == 0) {
-    float s = 0.f;
-    int c = 0;
-    for (int i = 0; i < W * R; ++i) {
-      s += zsum[i];
-      c += nsum[i];
-    }
-    out[2 * p.E] = s;
-    reinterpret_cast<int*>(out)[2 * p.E + 1] = c;
+  const int count = e < p.E ? hist[e] : 0;
+  if (B == 1) return finish_loss(p, P, count, z, c);
+  int* const counts = reinterpret_cast<int*>(p.work + (long long)B * p.E);
+  float* const zs = p.work + 2ll * B * p.E;
+  if (e < p.E) {
+    p.work[(long long)b * p.E + e] = P;
+    counts[(long long)b * p.E + e] = count;
+  }
+  if (e == 0) {
+    zs[b] = z;
+    reinterpret_cast<int*>(zs)[B + b] = c;
   }
 }
 
-__global__ __launch_bounds__(1024) void balance_final_kernel(RouterParams p, int blocks) {
-  __shared__ double dot[1024], num[1024];
-  __shared__ double z2;
-  __shared__ int tokens;
-  const int e = threadIdx.x, S = 2 * p.E + 2;
-  double P = 0, c = 0;
-  if (e < p.E) {
-    long long count = 0;
-    for (int b = 0; b < blocks; ++b) {
-      P += p.work[(long long)b * S + e];
-      count += reinterpret_cast<const int*>(p.work)[(long long)b * S + p.E + e];
-    }
-    c = (double)count;
-    p.counts_out[e] = (int)count;
-  }
-  dot[e] = c * P;
-  num[e] = c;
-  if (e == 0) {
+// Thread (slice, e) adds up every n-th workgroup's row from `slice` on; U rows
+// of both planes are in flight together.
+__global__ __launch_bounds__(kBalanceT) void balance_final_kernel(RouterParams p, int B, int slices) {
+  constexpr int U = 16;
+  __shared__ double sums[kBalanceT];
+  __shared__ int counts[kBalanceT];
+  __shared__ double zs[64];
+  __shared__ int ns[64];
+  const int width = kBalanceT / slices, e = threadIdx.x % width, s = threadIdx.x / width;
+  const int* const cplane = reinterpret_cast<const int*>(p.work + (long long)B * p.E);
+  const float* const zplane = p.work + 2ll * B * p.E;
+  if (threadIdx.x < 64) {
     double z = 0;
     int n = 0;
-    for (int b = 0; b < blocks; ++b) {
-      z += p.work[(long long)b * S + 2 * p.E];
-      n += reinterpret_cast<const int*>(p.work)[(long long)b * S + 2 * p.E + 1];
+    for (int b = threadIdx.x; b < B; b += 64) {
+      z += zplane[b];
+      n += reinterpret_cast<const int*>(zplane)[B + b];
     }
-    z2 = z;
-    tokens = n;
-    p.tokens_out[0] = n;
+    zs[threadIdx.x] = z;
+    ns[threadIdx.x] = n;
   }
+  double P = 0;
+  int count = 0;
+  if (e < p.E)
+    for (int b0 = s; b0 < B; b0 += U * slices) {
+      float f[U];
+      int c[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + u * slices < B ? b0 + u * slices : B - 1;
+        f[u] = p.work[(long long)b * p.E + e];
+        c[u] = cplane[(long long)b * p.E + e];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (b0 + u * slices < B) {
+          P += f[u];
+          count += c[u];
+        }
+    }
+  sums[threadIdx.x] = P;
+  counts[threadIdx.x] = count;
   __syncthreads();
-  for (int s = 512; s > 0; s >>= 1) {
-    if (e < s) {
-      dot[e] += dot[e + s];
-      num[e] += num[e + s];
+  double total = 0, z2 = 0;
+  int all = 0, n = 0;
+  if ((int)threadIdx.x < p.E)
+    for (int i = 0; i < slices; ++i) {
+      total += sums[i * width + threadIdx.x];
+      all += counts[i * width + threadIdx.x];
     }
-    __syncthreads();
-  }
-  if (e == 0) {
-    const double n = tokens > 0 ? tokens : 1, all = num[0] > 0 ? num[0] : 1;
-    p.loss_out[0] = (float)((double)p.coef * p.E * dot[0] / (all * n) + (double)p.z_coef * z2 / n);
-  }
+  if (threadIdx.x == 0)
+    for (int i = 0; i < 64; ++i) {
+      z2 += zs[i];
+      n += ns[i];
+    }
+  finish_loss(p, total, all, z2, n);
 }
 
 // ---------------------------------------------------------------------------
@@ -308,85 +490,110 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(RouterParams p, int
 //                  else u_j = scale s_j g_j
 //                  softmax: + u_j, and - s sum_j u_j for every expert where
 //                  not renormalised (the sum is 0 there); sigmoid: + u_j (1 - s_j)
+// The u_j go to their experts' lanes through a row of LDS a group.
 
-template <int L, int V>
+template <int L, int V, bool SIGMOID>
 __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
   constexpr int R = 64 / L, W = kRouterT / 64;
   __shared__ float picked[W * R][L * V];
   const int l = threadIdx.x & (L - 1), r = (threadIdx.x & 63) / L, w = threadIdx.x >> 6;
   const int lane0 = (threadIdx.x & 63) & ~(L - 1);
   float* const mine = picked[w * R + r];
+  const long long step = (long long)gridDim.x * (W * R);
+  long long t = (long long)blockIdx.x * (W * R) + w * R + r;
+  const long long end = p.T + w * R + r;
+  // A token's logits, and lane j's slot j; the next token's are asked for
+  // before the present one is worked on.
+  Row<V> next;
+  bool next_valid = load_row<L, V>(next, p, t, l);
+  long long next_id = -1;
+  float next_g = 0.f;
+  auto load_slot = [&](long long t1) __attribute__((always_inline)) {
+    next_id = load_id(p, t1, l);
+    if (next_id >= 0 && next_id < p.E)
+      next_g = load_value(p.dweights, t1 * p.k + l, p.dw_f32);
+    else
+      next_id = -1;
+  };
+  if (p.dweights) load_slot(t);
   float a[V], zfac = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    a[v] = 0.f;
-    mine[l + L * v] = 0.f;
-  }
+  for (int v = 0; v < V; ++v) a[v] = 0.f;
   if (p.counts) {
-    double c[V], all = 0;
+    int c[V];
+    double all = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = p.counts[l + L * v < p.E ? l + L * v : p.E - 1];
+    const int tokens = p.tokens[0];
+    const float up = p.dloss ? p.dloss[0] : 1.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      c[v] = l + L * v < p.E ? (double)p.counts[l + L * v] : 0.0;
+      if (l + L * v >= p.E) c[v] = 0;
       all += c[v];
     }
     all = group_sum<L>(all);
-    const int tokens = p.tokens[0];
-    const double up = (p.dloss ? (double)p.dloss[0] : 1.0) / (tokens > 0 ? tokens : 1);
+    const double n = tokens > 0 ? tokens : 1, per = (double)up * p.coef * p.E / ((all > 0 ? all : 1) * n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) a[v] = (float)(up * p.coef * p.E * c[v] / (all > 0 ? all : 1));
-    zfac = (float)(2 * up * p.z_coef);
+    for (int v = 0; v < V; ++v) a[v] = (float)(per * c[v]);
+    zfac = 2.f * up * p.z_coef / (float)n;
   }
-  for (long long t0 = (long long)blockIdx.x * (W * R); t0 < p.T; t0 += (long long)gridDim.x * (W * R)) {
-    const long long t = t0 + w * R + r;
-    Row<V> x = load_row<L, V>(p, t, l);
-    float soft[V], sum = 0.f;
+  for (; t < end; t += step) {
+    Row<V> x = next;
+    const bool valid = next_valid;
+    const int id = (int)next_id;
+    float g = next_g;
+    if (t + step < end) {
+      next_valid = load_row<L, V>(next, p, t + step, l);
+      if (p.dweights) load_slot(t + step);
+    }
+    row_state<L, V>(x, p, valid, l);
+    float z = -kInf;
+    if (p.dweights) {  // the chosen logits, from their lanes
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine[l + L * v] = x.z[v];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (id >= 0) z = mine[id];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine[l + L * v] = 0.f;
+    }
+    float s[V], soft[V], sum = 0.f, about = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      soft[v] = x.counts ? expf(x.z[v] - x.top) : 0.f;
+      soft[v] = exp_of(x.z[v] - x.top);
       sum += soft[v];
     }
     sum = group_sum<L>(sum);
-    const float lse = x.top + logf(sum);
-    float s[V], ssum = 0.f, about = 0.f;
+    const float over_sum = 1.f / sum, lse = x.top + logf(sum);
+    float over = over_sum;  // of the sum of the scores that soft or s hold
+    if constexpr (SIGMOID) {
+      float ssum = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      soft[v] = x.counts ? soft[v] / sum : 0.f;
-      s[v] = !p.sigmoid ? soft[v] : x.counts && x.z[v] > -kInf ? sigmoid(x.z[v]) : 0.f;
-      ssum += s[v];
-    }
-    if (p.sigmoid) ssum = group_sum<L>(ssum);
-    float pr[V];
+      for (int v = 0; v < V; ++v) {
+        s[v] = x.z[v] > -kInf ? sigmoid(x.z[v]) : 0.f;
+        ssum += s[v];
+        about = __builtin_fmaf(a[v], s[v], about);
+      }
+      ssum = group_sum<L>(ssum);
+      over = ssum > 0.f ? 1.f / ssum : 0.f;
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      pr[v] = !p.sigmoid ? s[v] : ssum > 0.f ? s[v] / ssum : 0.f;
-      about += a[v] * pr[v];
+      for (int v = 0; v < V; ++v) about = __builtin_fmaf(a[v], soft[v], about);
     }
-    about = group_sum<L>(about);
+    about = group_sum<L>(about) * over;
 
     float off = 0.f;
     if (p.dweights) {
-      // lane j takes slot j
-      int id = -1;
-      float g = 0.f, q = 0.f, z = -kInf;
-      if (x.counts && l < p.k) {
-        const long long i = t * p.k + l;
-        const long long e = p.ids64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
-        if (e >= 0 && e < p.E) {
-          id = (int)e;
-          g = load_value(p.dweights, i, p.dw_f32);
-          z = load_value(p.logits, t * p.E + id, p.x_f32);
-        }
-      }
-      const bool there = z > -kInf;  // (an expert that is switched off has score 0)
+      const bool there = x.counts && z > -kInf;  // (an expert that is switched off has score 0)
       if (!there) g = 0.f;
-      float not_q = 1.f;
-      if (p.sigmoid) {
-        q = there ? sigmoid(z) : 0.f;
-        not_q = there ? sigmoid(-z) : 0.f;
+      float q, not_q = 1.f;
+      if constexpr (SIGMOID) {
+        sigmoids(z, q, not_q);
+        if (!there) q = 0.f;
       } else {
         const float from = p.renorm ? group_max<L>(z) : x.top;
-        q = there ? expf(z - from) : 0.f;
-        if (!p.renorm) q = there ? q / sum : 0.f;
+        q = there ? exp_of(z - from) : 0.f;
+        if (!p.renorm) q *= over_sum;
       }
       if (p.renorm) {
         const float total = group_sum<L>(q);
@@ -394,107 +601,132 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
         g -= group_sum<L>(q * g);
       }
       float u = p.scale * q * g;
-      if (!p.sigmoid && !p.renorm) off = group_sum<L>(u);
+      if (!SIGMOID && !p.renorm) off = group_sum<L>(u);
       u *= not_q;
-      // slots of one expert are added up in their order, by the first of them
-      float total = 0.f;
+      // Every slot leaves its lane at its expert; where another lane's stands
+      // afterwards, slots of one expert meet, and are added up in their order
+      // by the first of them.
+      int* const owner = reinterpret_cast<int*>(mine);
       bool first = there;
-      for (int j = 0; j < p.k; ++j) {
-        const int other = __shfl(id, lane0 + j, 64);
-        const float uj = __shfl(u, lane0 + j, 64);
-        if (other == id) {
-          total += uj;
-          first = first && j >= l;
+      if (there) owner[id] = l;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const bool lost = there && owner[id] != l;
+      if (__ballot(lost) != 0) {
+        float total = 0.f;
+        for (int j = 0; j < p.k; ++j) {
+          const int other = __shfl(id, lane0 + j, 64);
+          const float uj = __shfl(u, lane0 + j, 64);
+          if (other == id) {
+            total += uj;
+            first = first && j >= l;
+          }
         }
+        u = total;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (first) mine[id] = total;
+      if (first) mine[id] = u;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
     }
+    float d[V];
+    const float c = p.counts ? zfac * lse : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = l + L * v;
-      float d = pr[v] * (a[v] - about);
-      if (p.sigmoid) d *= 1.f - s[v];
-      if (p.counts) d += zfac * lse * soft[v];
-      d -= off * soft[v];
-      if (p.dweights) {
-        d += mine[e];
-        mine[e] = 0.f;
-      }
-      if (x.bad) d = kNan;
-      if (!x.counts || x.z[v] == -kInf) d = 0.f;
-      if (t < p.T && e < p.E) {
-        if (p.x_f32)
-          static_cast<float*>(p.dlogits)[t * p.E + e] = d;
-        else
-          static_cast<uint16_t*>(p.dlogits)[t * p.E + e] = f32_to_bf16_rne(d);
+      if constexpr (SIGMOID)
+        d[v] = s[v] * over * (1.f - s[v]) * (a[v] - about) + soft[v] * over_sum * c;
+      else
+        d[v] = soft[v] * over_sum * (a[v] - about - off + c);
+      if (p.dweights) d[v] += mine[l + L * v];
+      if (x.bad) d[v] = kNan;
+      if (!x.counts || x.z[v] == -kInf) d[v] = 0.f;
+    }
+    if (t < p.T) {
+      if (p.x_f32) {
+        float* const out = static_cast<float*>(p.dlogits) + t * p.E;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (l + L * v < p.E) out[l + L * v] = d[v];
+      } else {
+        uint16_t* const out = static_cast<uint16_t*>(p.dlogits) + t * p.E;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (l + L * v < p.E) out[l + L * v] = f32_to_bf16_rne(d[v]);
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
-// Lanes and values a lane for E experts and k choices (a choice needs a lane).
-template <template <int, int> class F, class... A>
-hipError_t by_size(int E, int k, A... a) {
-  if (E <= 128 && k <= 16) {
-    if (E <= 16) return F<16, 1>::run(a...);
-    if (E <= 32) return F<16, 2>::run(a...);
-    if (E <= 64) return F<16, 4>::run(a...);
-    return F<16, 8>::run(a...);
-  }
-  if (E <= 128) return F<64, 2>::run(a...);
-  if (E <= 256) return F<64, 4>::run(a...);
-  if (E <= 512) return F<64, 8>::run(a...);
-  return F<64, 16>::run(a...);
-}
-
-int row_grid(const RouterParams& p, int L, int cu_count) {
+int row_grid(const RouterParams& p, int L, int cu_count, int per_cu) {
   const long long rows = (kRouterT / 64) * (64 / L);
   long long b = (p.T + rows - 1) / rows;
-  const long long most = (long long)cu_count * 8;
+  const long long most = (long long)cu_count * per_cu;
   return (int)(b < 1 ? 1 : b > most ? most : b);
 }
 
-template <int L, int V>
-struct Route {
-  static hipError_t run(const RouterParams* p, int cus, hipStream_t s) {
-    hipLaunchKernelGGL((route_kernel<L, V>), dim3(row_grid(*p, L, cus)), dim3(kRouterT), 0, s, *p);
-    return hipGetLastError();
-  }
-};
-template <int L, int V>
-struct Balance {
-  static hipError_t run(const RouterParams* p, int blocks, hipStream_t s) {
-    hipLaunchKernelGGL((balance_partial_kernel<L, V>), dim3(blocks), dim3(kRouterT), 0, s, *p);
-    return hipGetLastError();
-  }
-};
-template <int L, int V>
-struct Grad {
-  static hipError_t run(const RouterParams* p, int cus, hipStream_t s) {
-    hipLaunchKernelGGL((router_grad_kernel<L, V>), dim3(row_grid(*p, L, cus)), dim3(kRouterT), 0, s, *p);
-    return hipGetLastError();
-  }
-};
-
-}  // namespace
-
-hipError_t launch_route(const RouterParams& p, int cu_count, hipStream_t stream) {
-  return by_size<Route>(p.E, p.k, &p, cu_count, stream);
+template <int L, int V, bool K8>
+hipError_t route(const RouterParams& p, int cus, hipStream_t s) {
+  hipLaunchKernelGGL((route_kernel<L, V, K8>), dim3(row_grid(p, L, cus, 8)), dim3(kRouterT), 0, s, p);
+  return hipGetLastError();
 }
-
-hipError_t launch_balance_loss(const RouterParams& p, int blocks, hipStream_t stream) {
-  const hipError_t e = by_size<Balance>(p.E, p.k, &p, blocks, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_final_kernel, dim3(1), dim3(1024), 0, stream, p, blocks);
+template <int L, int V>
+hipError_t balance(const RouterParams& p, int blocks, hipStream_t s) {
+  hipLaunchKernelGGL((balance_partial_kernel<L, V>), dim3(blocks), dim3(kBalanceT), 0, s, p);
+  return hipGetLastError();
+}
+template <int L, int V>
+hipError_t grad(const RouterParams& p, int cus, hipStream_t s) {
+  if (p.sigmoid)
+    hipLaunchKernelGGL((router_grad_kernel<L, V, true>), dim3(row_grid(p, L, cus, 4)), dim3(kRouterT), 0, s, p);
+  else
+    hipLaunchKernelGGL((router_grad_kernel<L, V, false>), dim3(row_grid(p, L, cus, 4)), dim3(kRouterT), 0, s, p);
   return hipGetLastError();
 }
 
-hipError_t launch_router_grad(const RouterParams& p, int cu_count, hipStream_t stream) {
-  return by_size<Grad>(p.E, p.k, &p, cu_count, stream);
+}  // namespace
+
+hipError_t launch_route(const RouterParams& p, int cus, hipStream_t s) {
+  const int E = p.E;
+  if (p.k <= 8) {
+    if (E <= 64) return route<8, 8, true>(p, cus, s);
+    if (E <= 128) return route<8, 16, true>(p, cus, s);
+    if (E <= 256) return route<16, 16, true>(p, cus, s);
+    if (E <= 512) return route<64, 8, true>(p, cus, s);
+    return route<64, 16, true>(p, cus, s);
+  }
+  // (a choice needs a lane)
+  if (E <= 128 && p.k <= 16) return route<16, 8, false>(p, cus, s);
+  if (E <= 128) return route<64, 2, false>(p, cus, s);
+  if (E <= 256) return route<64, 4, false>(p, cus, s);
+  if (E <= 512) return route<64, 8, false>(p, cus, s);
+  return route<64, 16, false>(p, cus, s);
+}
+
+hipError_t launch_balance_loss(const RouterParams& p, int blocks, hipStream_t s) {
+  const int E = p.E;
+  const hipError_t e = E <= 32 ? balance<16, 2>(p, blocks, s)
+                       : E <= 64 ? balance<16, 4>(p, blocks, s)
+                       : E <= 128 ? balance<16, 8>(p, blocks, s)
+                       : E <= 256 ? balance<64, 4>(p, blocks, s)
+                       : E <= 512 ? balance<64, 8>(p, blocks, s)
+                                  : balance<64, 16>(p, blocks, s);
+  if (e != hipSuccess || blocks == 1) return e;
+  int slices = 1;
+  while (slices < 32 && E * slices * 2 <= kBalanceT) slices *= 2;
+  hipLaunchKernelGGL(balance_final_kernel, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_grad(const RouterParams& p, int cus, hipStream_t s) {
+  const int E = p.E;
+  if (E <= 128 && p.k <= 16) {
+    if (E <= 32) return grad<16, 2>(p, cus, s);
+    if (E <= 64) return grad<16, 4>(p, cus, s);
+    return grad<16, 8>(p, cus, s);
+  }
+  if (E <= 128) return grad<64, 2>(p, cus, s);
+  if (E <= 256) return grad<64, 4>(p, cus, s);
+  if (E <= 512) return grad<64, 8>(p, cus, s);
+  return grad<64, 16>(p, cus, s);
 }
 
 }  // namespace gmmk

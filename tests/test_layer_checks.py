@@ -85,13 +85,16 @@ def test_route(lib):
 
 
 def test_balance_loss(lib):
-    need = lib.balance_bytes(ctypes.c_longlong(5), ctypes.c_longlong(16))
-    ok = [tensor(A, F32, 5, 16), tensor(B, I64, 5, 4), None, 0, tensor(C, F32, 1), tensor(D, I32, 16), tensor(E, I32, 1),
+    need = lib.balance_bytes(ctypes.c_longlong(500), ctypes.c_longlong(16))
+    ok = [tensor(A, F32, 500, 16), tensor(B, I64, 500, 4), None, 0, tensor(C, F32, 1), tensor(D, I32, 16), tensor(E, I32, 1),
           P(F), ctypes.c_size_t(need)]
     good(lib, "balance", *ok)
-    good(lib, "balance", *swapped(ok, a1=tensor(B, I32, 5, 4), a2=tensor(H, I8, 5)))
+    good(lib, "balance", *swapped(ok, a1=tensor(B, I32, 500, 4), a2=tensor(H, I8, 500)))
+    # one workgroup needs none
+    assert lib.balance_bytes(ctypes.c_longlong(64), ctypes.c_longlong(16)) == 0 == lib.balance_bytes(ctypes.c_longlong(0), ctypes.c_longlong(1024))
+    good(lib, "balance", *swapped(ok, a0=tensor(A, F32, 64, 16), a1=tensor(B, I64, 64, 4), a7=P(None), a8=ctypes.c_size_t(0)))
     for status, word, kw in (
-            (INVALID, "required", dict(a6=None)), (INVALID, "int32 or int64", dict(a1=tensor(B, F32, 5, 4))),
+            (INVALID, "required", dict(a6=None)), (INVALID, "int32 or int64", dict(a1=tensor(B, F32, 500, 4))),
             (INVALID, "loss", dict(a4=tensor(C, F32, 2))), (INVALID, "loss", dict(a4=tensor(C, BF16, 1))),
             (INVALID, "counts", dict(a5=tensor(D, I32, 15))), (INVALID, "tokens", dict(a6=tensor(E, I64, 1))),
             (INVALID, "overlaps an input", dict(a5=tensor(A, I32, 16))), (INVALID, "two outputs", dict(a6=tensor(D, I32, 1))),

@@ -151,7 +151,7 @@ gmm_status gmm_router_grad_run(gmm_handle* h,
 
 /*
  * gmm_gmv_workspace: bytes of workspace that gmm_gmv_run needs for a product
- * of `slots` = T*k rows to N columns (0 without weights).
+ * of `slots` = T*k rows to N columns (0 without weights, and for a few slots).
  */
 gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* bytes);
 
@@ -176,7 +176,7 @@ gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* byt
  *   weights     NULL or [T,k], F32 or BF16.
  *   out         [T,k,N], with weights [T,N]; F32 or BF16.
  * Limits: T*k <= 4096 (more rows belong to gmm_run), 1 <= k <= 64,
- * G <= 1024, N and K below 2^24 (GMM_E_UNSUPPORTED above).
+ * G <= 1024, N < 2^24, K < 2^20 (GMM_E_UNSUPPORTED above).
  */
 gmm_status gmm_gmv_run(gmm_handle* h,
                        const gmm_tensor* x,

@@ -26,11 +26,12 @@ HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                "-Wno-unused-command-line-argument"]
 
-# Per-source additions: the block-scaled fp8 kernel and the weight-streaming
-# kernel keep their MFMA results in ordinary VGPRs, where their scale folds
+# Per-source additions: the block-scaled fp8 kernel, the weight-streaming kernel
+# and the products by expert id keep their MFMA results in ordinary VGPRs, where their scale folds
 # read them.
 EXTRA_FLAGS = {"gmm_w8a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "gmm_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "gmm_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "gmm_gmv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

@@ -14,7 +14,8 @@
 namespace gmmh {
 
 constexpr long long kMaxGmvSlots = 4096;
-constexpr long long kMaxGmvExtent = 1LL << 24;
+constexpr long long kMaxGmvCols = 1LL << 24;
+constexpr long long kMaxGmvK = 1LL << 20;
 constexpr long long kMaxAdamElems = 1LL << 40;
 
 // logits [T,E], ids [T,k] of the given types, valid [T].
@@ -110,14 +111,18 @@ inline Check check_router_grad(const gmm_tensor* logits, const gmm_tensor* ids, 
   return check_memory({logits, ids, valid, dweights, counts, tokens, dloss}, {dlogits});
 }
 
+// Up to so many slots the weighted sums are taken in one launch, without a
+// workspace.
+constexpr long long kGmvAtOnce = 16;
+
 inline size_t gmv_workspace_bytes(long long slots, long long N, bool weighted) {
-  return weighted ? (size_t)slots * (size_t)N * sizeof(float) : 0;
+  return weighted && slots > kGmvAtOnce ? (size_t)slots * (size_t)N * sizeof(float) : 0;
 }
 
 inline Check check_gmv_limits(long long slots, long long N) {
   if (slots < 0 || N < 1) return invalid("negative or zero extent");
   if (slots > kMaxGmvSlots) return unsupported("more than 4096 slots (T*k): gmm_run takes sorted rows");
-  if (N >= kMaxGmvExtent) return unsupported("2^24 columns or more");
+  if (N >= kMaxGmvCols) return unsupported("2^24 columns or more");
   return {};
 }
 
@@ -131,7 +136,7 @@ inline Check check_gmv(const gmm_tensor* x, const gmm_tensor* rhs, const gmm_ten
     return invalid("expected rhs of shape (G, N, K), got " + shape_str(rhs));
   const long long G = rhs->shape[0], N = rhs->shape[1], K = rhs->shape[2];
   if (G > gmmk::kMaxGroups) return unsupported("more than 1024 groups");
-  if (K >= kMaxGmvExtent) return unsupported("K of 2^24 or more");
+  if (K >= kMaxGmvK) return unsupported("K of 2^20 or more");
   if (K % 32) return invalid("K must be a multiple of 32");
   long long T, k;
   Check c;

@@ -53,7 +53,15 @@ struct GmvParams {
   int32_t T, k, n, G, N, K, nb, blk;
   int32_t fmt;  // 3 int4, 4 uint4, 5 fp4 e2m1
   int32_t scale_kind, ids64, w_f32, out_f32, per_slot;
+  int32_t experts;     // most experts that the slots can choose: min(n, G)
+  uint32_t blk_magic;  // block b of 32 elements lies in scale block b * blk_magic >> 31
+  int32_t at_once;     // the weighted sums are taken in one launch, without the workspace
 };
+// For scale blocks of d * 32 elements: ceil(2^31 / d), exact for b d < 2^31.
+inline uint32_t gmv_magic(int blk) {
+  const uint64_t d = (uint64_t)blk / 32;
+  return (uint32_t)(((1ull << 31) + d - 1) / d);
+}
 hipError_t launch_gmv(const GmvParams& p, int cu_count, hipStream_t stream);
 
 // AdamW: up to kAdamItems tensors a launch, cut into chunks.

@@ -131,7 +131,9 @@ def test_gmv(lib):
     good(lib, "gmv", *swapped(ok, a0=tensor(A, BF16, 3, 2, 64), a1=tensor(B, U4, 5, 24, 64), a4=tensor(E, I64, 3, 2)))
     good(lib, "gmv", *swapped(ok, a2=tensor(C, BF16, 5, 1, 1, 24), a3=tensor(D, BF16, 5, 1, 1, 24)))
     good(lib, "gmv", *swapped(ok, a1=tensor(B, F4, 5, 24, 64), a2=tensor(C, E8M0, 5, 2, 1, 24), a3=None))
-    weighted = swapped(ok, a5=tensor(H, F32, 3, 2), a6=tensor(F, BF16, 3, 24), a7=P(I), a8=ctypes.c_size_t(3 * 2 * 24 * 4))
+    few = swapped(ok, a5=tensor(H, F32, 3, 2), a6=tensor(F, BF16, 3, 24))  # (no workspace)
+    good(lib, "gmv", *few)
+    weighted = swapped(gmv_args(T=9), a5=tensor(H, F32, 9, 2), a6=tensor(F, BF16, 9, 24), a7=P(I), a8=ctypes.c_size_t(9 * 2 * 24 * 4))
     good(lib, "gmv", *weighted)
     dense = swapped(gmv_args(T=7, k=1, G=1), a4=None)
     good(lib, "gmv", *dense)
@@ -141,7 +143,7 @@ def test_gmv(lib):
             (INVALID, "required", dict(a2=None)), (INVALID, "x must be bf16", dict(a0=tensor(A, F32, 3, 64))),
             (INVALID, "int4, uint4", dict(a1=tensor(B, I8, 5, 24, 64))), (INVALID, "(G, N, K)", dict(a1=tensor(B, I4, 24, 64))),
             (INVALID, "(G, N, K)", dict(a1=tensor(B, I4, 5, 0, 64))), (UNSUPPORTED, "1024 groups", dict(a1=tensor(B, I4, 1025, 24, 64))),
-            (INVALID, "multiple of 32", dict(a1=tensor(B, I4, 5, 24, 48))), (UNSUPPORTED, "2^24", dict(a1=tensor(B, I4, 5, 24, 1 << 24))),
+            (INVALID, "multiple of 32", dict(a1=tensor(B, I4, 5, 24, 48))), (UNSUPPORTED, "2^20", dict(a1=tensor(B, I4, 5, 24, 1 << 20))),
             (UNSUPPORTED, "2^24", dict(a1=tensor(B, I4, 5, 1 << 24, 64))), (INVALID, "int32 or int64", dict(a4=tensor(E, F32, 3, 2))),
             (INVALID, "expert_ids are required", dict(a4=None)), (UNSUPPORTED, "64 choices", dict(a4=tensor(E, I32, 3, 65))),
             (UNSUPPORTED, "4096 slots", dict(a4=tensor(E, I32, 2049, 2))), (INVALID, "x of shape", dict(a0=tensor(A, BF16, 4, 64))),
@@ -156,8 +158,8 @@ def test_gmv(lib):
             (INVALID, "(T, k, N)", dict(a6=tensor(F, F32, 3, 24))), (INVALID, "overlaps an input", dict(a6=tensor(A, F32, 3, 2, 24))),
             (INVALID, "null", dict(a0=tensor(None, BF16, 3, 64))), (INVALID, "16-byte", dict(a1=tensor(B + 8, I4, 5, 24, 64)))):
         refused(lib, status, word, "gmv", *swapped(ok, **kw))
-    for status, word, kw in ((INVALID, "(T, N)", dict(a6=tensor(F, BF16, 3, 2, 24))), (INVALID, "weights", dict(a5=tensor(H, F32, 2, 3))),
-                             (INVALID, "weights", dict(a5=tensor(H, I32, 3, 2))), (INVALID, "workspace needs", dict(a7=P(None))),
+    for status, word, kw in ((INVALID, "(T, N)", dict(a6=tensor(F, BF16, 9, 2, 24))), (INVALID, "weights", dict(a5=tensor(H, F32, 2, 9))),
+                             (INVALID, "weights", dict(a5=tensor(H, I32, 9, 2))), (INVALID, "workspace needs", dict(a7=P(None))),
                              (INVALID, "workspace overlaps", dict(a7=P(F))), (INVALID, "16-byte", dict(a7=P(I + 4)))):
         refused(lib, status, word, "gmv", *swapped(weighted, **kw))
 
@@ -237,7 +239,8 @@ def test_library_exports_the_header():
     assert "#define GMM_SCORES_SOFTMAX 0\n" in text and "#define GMM_SCORES_SIGMOID 1\n" in text
     need = ctypes.c_size_t(7)
     assert lib.gmm_gmv_workspace(8, 1408, 0, ctypes.byref(need)) == OK and need.value == 0
-    assert lib.gmm_gmv_workspace(8, 1408, 1, ctypes.byref(need)) == OK and need.value <= 8 * 1408 * 4
+    assert lib.gmm_gmv_workspace(8, 1408, 1, ctypes.byref(need)) == OK and need.value == 0
+    assert lib.gmm_gmv_workspace(80, 1408, 1, ctypes.byref(need)) == OK and need.value == 80 * 1408 * 4
     assert lib.gmm_gmv_workspace(4097, 1408, 1, ctypes.byref(need)) == UNSUPPORTED
     assert lib.gmm_gmv_workspace(-1, 1408, 1, ctypes.byref(need)) == INVALID
     assert lib.gmm_balance_loss_workspace(32768, 128, ctypes.byref(need)) == OK and need.value < 1 << 20

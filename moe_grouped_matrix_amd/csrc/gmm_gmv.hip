@@ -22,8 +22,11 @@
 // that is 8 more, and a zero point 8 higher).  fp4 codes have a conversion of
 // their own, which takes an E8M0 scale along (exact, no fold).
 //
-// With up to four rows, row r sits in row 4 r of the product, whose result is
-// then one register a lane: a quarter of the folds.
+// With up to four rows (FEW) one load and one operand bring a chunk's x: row
+// 4 r + j of the operand is row r's block j.  The product with block i's
+// weights then has the wanted sum in row 4 r + i, which is register i of lane
+// group r; the other rows are blocks that do not belong together, and are left
+// alone.  One product with ones gives the sums of x of all four blocks.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -117,12 +120,12 @@ __device__ __forceinline__ i32x4 spread4(int v) {
 
 // One chunk of 128 elements of K: the lane's codes of NT column tiles, its
 // scales and zero points (of its own block of 32), and its x elements of the
-// four blocks.
-template <int NT>
+// four blocks (FEW: of one of them).
+template <int NT, bool FEW>
 struct Chunk {
   i32x4 w[NT];
   int s[NT], z[NT];
-  i32x4 x[4];
+  i32x4 x[FEW ? 1 : 4];
 };
 
 // What a wave reads for one expert.
@@ -135,8 +138,8 @@ struct Source {
   const uint16_t* x;  // the lane's row of x
 };
 
-template <Kind KIND, int NT>
-__device__ __forceinline__ void load_chunk(Chunk<NT>& d, const GmvParams& p, const Source<NT>& src, int c, int q) {
+template <Kind KIND, int NT, bool FEW>
+__device__ __forceinline__ void load_chunk(Chunk<NT, FEW>& d, const GmvParams& p, const Source<NT>& src, int c, int q) {
   const int k0 = 128 * c, mine = k0 + 32 * q < p.K ? k0 + 32 * q : k0;  // (past K: read elsewhere, and not used)
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -156,26 +159,50 @@ __device__ __forceinline__ void load_chunk(Chunk<NT>& d, const GmvParams& p, con
       if (p.zero)
         d.z[t] = p.scale_kind == kGmvF32 ? static_cast<const int*>(p.zero)[i] : static_cast<const uint16_t*>(p.zero)[i] << 16;
   }
+  if constexpr (FEW) {
+    const int i = threadIdx.x & 3, k = k0 + 32 * i < p.K ? k0 + 32 * i : k0;
+    d.x[0] = *reinterpret_cast<const i32x4*>(src.x + k + 8 * q);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = k0 + 32 * i < p.K ? k0 + 32 * i : k0;
-    d.x[i] = *reinterpret_cast<const i32x4*>(src.x + k + 8 * q);
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 32 * i < p.K ? k0 + 32 * i : k0;
+      d.x[i] = *reinterpret_cast<const i32x4*>(src.x + k + 8 * q);
+    }
   }
 }
 
-// tot[t][r] += the chunk's products; REGS result registers count (one with up
-// to four rows).  WHOLE: the four blocks share their scale (blocks are
-// multiples of 128).  weight: of the whole sum (1, or a router's).
-template <Kind KIND, bool WHOLE, bool WEIGHTED, int NT, int REGS>
-__device__ __forceinline__ void use_chunk(float (&tot)[NT][REGS], f32x4 (&run)[NT], Chunk<NT>& d, const GmvParams& p, int c,
-                                          float weight) {
+// The wave's sums: tot[t][r] of lane (q, n) for column n of tile t and row q
+// (FEW) or 4 q + r.  fp4 with E8M0 scales needs no folds, and sums in the matrix
+// cores' results, run (FEW: one for each block of a chunk).
+template <int NT, bool FEW>
+struct Sums {
+  float tot[NT][FEW ? 1 : 4];
+  f32x4 run[NT][FEW ? 4 : 1];
+};
+
+template <int NT, bool FEW>
+__device__ __forceinline__ void clear(Sums<NT, FEW>& a) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (float& v : a.tot[t]) v = 0.f;
+#pragma unroll
+    for (f32x4& v : a.run[t]) v = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// Adds the products of chunk c.  WHOLE: its four blocks share their scale (scale
+// blocks are multiples of 128).  WEIGHTED: times `weight`.
+template <Kind KIND, bool WHOLE, bool WEIGHTED, int NT, bool FEW>
+__device__ __forceinline__ void use_chunk(Sums<NT, FEW>& a, Chunk<NT, FEW>& d, const GmvParams& p, int c, float weight) {
   const int left = (p.K >> 5) - 4 * c;  // blocks from here on
   const f32x4 none{0.f, 0.f, 0.f, 0.f};
   const i32x4 one4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
   const float base = KIND == kInt && p.fmt == 3 ? 8.f : 0.f;
   const int flip = KIND == kInt && p.fmt == 3 ? (int)0x88888888u : 0;
-  constexpr bool CHAIN = KIND == kMicro && !WEIGHTED;  // sums stay in the matrix cores' registers to the end
+  constexpr bool CHAIN = KIND == kMicro && !WEIGHTED;
+  constexpr int ROWS = FEW ? 1 : 4;
   i32x4 s4[NT], z4[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -187,47 +214,73 @@ __device__ __forceinline__ void use_chunk(float (&tot)[NT][REGS], f32x4 (&run)[N
         if (p.zero) z4[t] = spread4(d.z[t]);
     }
   }
-  f32x4 acc[NT], sum = none;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = none;
-  auto fold = [&](int t, float scale, float zero) __attribute__((always_inline)) {
-    if constexpr (WEIGHTED) scale *= weight;
-#pragma unroll
-    for (int r = 0; r < REGS; ++r) {
-      const float v = KIND == kInt ? __builtin_fmaf(-zero, sum[r], acc[t][r]) : acc[t][r];
-      tot[t][r] = __builtin_fmaf(scale, v, tot[t][r]);
-    }
+  // sums of products `got` and of x `sum`, for row r
+  auto fold = [&](int t, int r, float got, float sum, int scale, int zero) __attribute__((always_inline)) {
+    float s = KIND == kMicro ? 1.f : __int_as_float(scale);
+    if constexpr (WEIGHTED) s *= weight;
+    if constexpr (KIND == kInt) got = __builtin_fmaf(-(p.zero ? __int_as_float(zero) + base : base), sum, got);
+    a.tot[t][r] = __builtin_fmaf(s, got, a.tot[t][r]);
   };
+  f32x4 acc[NT], sum = none;
+  float few[NT], few_sum = 0.f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    acc[t] = none;
+    few[t] = 0.f;
+  }
+  bf16x8 x = ordered_x<KIND>(d.x[0]);
+  if constexpr (FEW && KIND == kInt) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, none, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (i >= left) break;
-    const bf16x8 x = ordered_x<KIND>(d.x[i]);
-    if constexpr (KIND == kInt) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, WHOLE ? sum : none, 0, 0, 0);
+    if constexpr (!FEW) {
+      if (i > 0) x = ordered_x<KIND>(d.x[i]);
+      if constexpr (KIND == kInt) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, WHOLE ? sum : none, 0, 0, 0);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const bf16x8 w = widen8<KIND>((unsigned)d.w[t][i], KIND == kMicro ? s4[t][i] : 0);
       if constexpr (CHAIN) {
-        run[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, run[t], 0, 0, 0);
-      } else if constexpr (WHOLE || KIND == kMicro) {
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, acc[t], 0, 0, 0);
-      } else {
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, none, 0, 0, 0);
-        fold(t, __int_as_float(s4[t][i]), KIND == kInt ? (p.zero ? __int_as_float(z4[t][i]) + base : base) : 0.f);
+        f32x4& run = a.run[t][FEW ? i : 0];
+        run = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, run, 0, 0, 0);
+        continue;
+      }
+      constexpr bool TOGETHER = WHOLE || KIND == kMicro;
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, TOGETHER && !FEW ? acc[t] : none, 0, 0, 0);
+      if constexpr (!TOGETHER) {
+        if constexpr (FEW) {
+          fold(t, 0, acc[t][i], sum[i], s4[t][i], z4[t][i]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) fold(t, r, acc[t][r], sum[r], s4[t][i], z4[t][i]);
+        }
+      } else if constexpr (FEW) {
+        few[t] += acc[t][i];
       }
     }
+    if constexpr (FEW && WHOLE) few_sum += sum[i];
   }
   if constexpr (!CHAIN && (WHOLE || KIND == kMicro)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      fold(t, KIND == kMicro ? 1.f : __int_as_float(d.s[t]), KIND == kInt ? (p.zero ? __int_as_float(d.z[t]) + base : base) : 0.f);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) fold(t, r, FEW ? few[t] : acc[t][r], FEW ? few_sum : sum[r], d.s[t], d.z[t]);
   }
 }
 
-// The slots of the r-th expert (in the order of their numbers) that any slot
-// chose: into list, for every wave of the workgroup; returns how many, and the
-// expert.  Up to 64 slots each wave looks for itself: equal ids find each other
-// by a ballot per bit of the id, and an expert's first slot stands for it (the
-// r-th first slot, then: the order does not matter).
+// What the sums came to.
+template <Kind KIND, bool WEIGHTED, int NT, bool FEW>
+__device__ __forceinline__ float total(const Sums<NT, FEW>& a, int t, int r) {
+  if constexpr (KIND != kMicro || WEIGHTED) return a.tot[t][r];
+  if constexpr (FEW) return (a.run[t][0][0] + a.run[t][1][1]) + (a.run[t][2][2] + a.run[t][3][3]);
+  return a.run[t][0][r];
+}
+
+// The slots of the r-th expert that any slot chose: into list; returns how
+// many, and the expert (-1: fewer than r + 1 were chosen).  In which order the
+// experts are counted, and the slots listed, does not matter.  Up to 64 slots
+// each wave looks for itself: equal ids find each other by a ballot per bit of
+// the id, and an expert's first slot stands for it.
 struct Found {
   int expert, count;
 };
@@ -253,6 +306,30 @@ __device__ __forceinline__ Found find_few(const GmvParams& p, int r, uint16_t* l
   if (id == g) list[__builtin_popcountll(mine & below)] = (uint16_t)lane;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   return {g, (int)__builtin_popcountll(mine)};
+}
+
+// The slots of expert g; every wave looks through all ids for itself (and
+// writes the same list), eight of them a lane at a time.
+__device__ __forceinline__ Found find_slots(const GmvParams& p, int g, uint16_t* list) {
+  const int lane = threadIdx.x & 63;
+  const unsigned long long below = (1ull << lane) - 1;
+  int count = 0;
+  for (int i0 = 0; i0 < p.n; i0 += 512) {
+    int id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + 64 * u + lane;
+      id[u] = i < p.n ? slot_expert(p, i) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const unsigned long long mine = __ballot(id[u] == g);
+      if (id[u] == g) list[count + __builtin_popcountll(mine & below)] = (uint16_t)(i0 + 64 * u + lane);
+      count += __builtin_popcountll(mine);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return {count ? g : -1, count};
 }
 
 template <int T>
@@ -311,26 +388,20 @@ __device__ __forceinline__ void set_columns(Source<NT>& src, const GmvParams& p,
   }
 }
 
-// One pass over the expert's columns for rows list[first ..]: REGS as in use_chunk.
-template <Kind KIND, bool WHOLE, int NT, int REGS, int W>
+// One pass over the expert's columns for rows list[first ..].
+template <Kind KIND, bool WHOLE, int NT, bool FEW, int W>
 __device__ __forceinline__ void pass(const GmvParams& p, Source<NT>& src, const uint16_t* list, int first, int rows, int n0,
                                      float* join) {
   constexpr int D = NT == 1 ? 3 : 2;  // chunks in flight
-  constexpr int ROWS = 4 * REGS;
+  constexpr int ROWS = FEW ? 4 : 16;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, n = lane & 15;
-  const int row = REGS == 1 ? n >> 2 : n;
+  const int row = FEW ? n >> 2 : n;
   const int slot = list[first + (row < rows ? row : 0)];
   src.x = p.x + (long long)(p.per_slot ? slot : slot / p.k) * p.K;
   const int chunks = (p.K + 127) >> 7, lo = chunks * w / W, hi = chunks * (w + 1) / W;
-  float tot[NT][REGS];
-  f32x4 run[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    run[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < REGS; ++r) tot[t][r] = 0.f;
-  }
-  Chunk<NT> d[D];
+  Sums<NT, FEW> sums;
+  clear(sums);
+  Chunk<NT, FEW> d[D];
 #pragma unroll
   for (int i = 0; i < D; ++i)
     if (lo + i < hi) load_chunk<KIND>(d[i], p, src, lo + i, q);
@@ -338,7 +409,7 @@ __device__ __forceinline__ void pass(const GmvParams& p, Source<NT>& src, const 
 #pragma unroll
     for (int i = 0; i < D; ++i)
       if (c + i < hi) {
-        use_chunk<KIND, WHOLE, false, NT, REGS>(tot, run, d[i], p, c + i, 1.f);
+        use_chunk<KIND, WHOLE, false>(sums, d[i], p, c + i, 1.f);
         if (c + i + D < hi) load_chunk<KIND>(d[i], p, src, c + i + D, q);
       }
   }
@@ -346,8 +417,8 @@ __device__ __forceinline__ void pass(const GmvParams& p, Source<NT>& src, const 
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < REGS; ++r)
-      join[(w * ROWS + (REGS == 1 ? q : 4 * q + r)) * (16 * NT) + 16 * t + n] = KIND == kMicro ? run[t][r] : tot[t][r];
+    for (int r = 0; r < ROWS / 4; ++r)
+      join[(w * ROWS + (FEW ? q : 4 * q + r)) * (16 * NT) + 16 * t + n] = total<KIND, false>(sums, t, r);
   __syncthreads();
   for (int i = threadIdx.x; i < rows * 16 * NT; i += 64 * W) {
     const int rr = i / (16 * NT), col = i % (16 * NT);
@@ -366,7 +437,7 @@ __device__ __forceinline__ void pass(const GmvParams& p, Source<NT>& src, const 
 }
 
 template <Kind KIND, bool WHOLE, int NT>
-__global__ __launch_bounds__(256) void gmv_kernel(GmvParams p) {
+__global__ __launch_bounds__(256, 4) void gmv_kernel(GmvParams p) {
   constexpr int W = 4;
   __shared__ uint16_t list[kMaxSlots];
   __shared__ float join[W * 16 * 16 * NT];
@@ -378,7 +449,9 @@ __global__ __launch_bounds__(256) void gmv_kernel(GmvParams p) {
     }
     return;
   }
-  const Found f = p.n <= 64 ? find_few(p, blockIdx.y, list) : find_many<64 * W>(p, blockIdx.y, list);
+  const Found f = p.n <= 64 ? find_few(p, blockIdx.y, list)
+                  : p.experts == p.G ? find_slots(p, blockIdx.y, list)
+                                     : find_many<64 * W>(p, blockIdx.y, list);
   if (f.expert < 0) return;
   Source<NT> src;
   set_columns(src, p, n0, n);
@@ -387,9 +460,9 @@ __global__ __launch_bounds__(256) void gmv_kernel(GmvParams p) {
   for (int first = 0; first < f.count; first += 16) {
     const int rows = f.count - first < 16 ? f.count - first : 16;
     if (rows <= 4)
-      pass<KIND, WHOLE, NT, 1, W>(p, src, list, first, rows, n0, join);
+      pass<KIND, WHOLE, NT, true, W>(p, src, list, first, rows, n0, join);
     else
-      pass<KIND, WHOLE, NT, 4, W>(p, src, list, first, rows, n0, join);
+      pass<KIND, WHOLE, NT, false, W>(p, src, list, first, rows, n0, join);
   }
 }
 
@@ -418,12 +491,12 @@ __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
   set_columns(src, p, n0, n);
   const int chunks = (p.K + 127) >> 7, all = __builtin_popcountll(live) * chunks;
   const int lo = all * w / W, hi = all * (w + 1) / W;
-  float tot[1][1] = {{0.f}};
-  f32x4 run[1];
+  Sums<1, true> sums;
+  clear(sums);
   constexpr int D = 3;
-  Chunk<1> d[D];
+  Chunk<1, true> d[D];
   float weight[D];
-  auto load = [&](Chunk<1>& into, float& wt, int item) __attribute__((always_inline)) {
+  auto load = [&](Chunk<1, true>& into, float& wt, int item) __attribute__((always_inline)) {
     const int j = item / chunks;
     const int g = __builtin_amdgcn_readfirstlane(expert[j]), i = __builtin_amdgcn_readfirstlane(slot[j]);
     src.w = p.rhs + (long long)g * p.N * (p.K / 2);
@@ -439,11 +512,11 @@ __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
 #pragma unroll
     for (int i = 0; i < D; ++i)
       if (c + i < hi) {
-        use_chunk<KIND, WHOLE, true, 1, 1>(tot, run, d[i], p, (c + i) % chunks, weight[i]);
+        use_chunk<KIND, WHOLE, true>(sums, d[i], p, (c + i) % chunks, weight[i]);
         if (c + i + D < hi) load(d[i], weight[i], c + i + D);
       }
   }
-  if (q == 0) join[w][n] = tot[0][0];
+  if (q == 0) join[w][n] = total<KIND, true>(sums, 0, 0);
   __syncthreads();
   if (threadIdx.x < 16 && n0 + n < p.N) {
     float v = 0.f;
@@ -473,8 +546,8 @@ hipError_t launch(const GmvParams& p, int cu_count, hipStream_t s) {
     return hipGetLastError();
   }
   const unsigned experts = p.experts + (p.weights ? 0 : 1);
-  if ((long long)((p.N + 63) / 64) * p.experts >= 2 * cu_count)
-    hipLaunchKernelGGL((gmv_kernel<KIND, WHOLE, 4>), dim3((p.N + 63) / 64, experts), dim3(256), 0, s, p);
+  if ((long long)((p.N + 31) / 32) * p.experts >= 2 * cu_count)
+    hipLaunchKernelGGL((gmv_kernel<KIND, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(256), 0, s, p);
   else
     hipLaunchKernelGGL((gmv_kernel<KIND, WHOLE, 1>), dim3((p.N + 15) / 16, experts), dim3(256), 0, s, p);
   if (p.weights) hipLaunchKernelGGL(gmv_join_kernel, dim3((p.N + 255) / 256, p.T), dim3(256), 0, s, p);

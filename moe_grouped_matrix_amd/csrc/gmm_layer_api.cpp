@@ -175,7 +175,7 @@ gmm_status gmm_gmv_run(gmm_handle* h, const gmm_tensor* x, const gmm_tensor* rhs
         p.out = written<void>(out);
         p.out_f32 = out->dtype == GMM_F32;
         p.work = static_cast<float*>(workspace);
-        p.experts = p.n < p.G ? p.n : p.G;
+        p.experts = 2 * p.n < p.G || p.n <= 64 ? (p.n < p.G ? p.n : p.G) : p.G;
         p.blk_magic = gmmk::gmv_magic(p.blk);
         p.at_once = p.weights && p.n <= kGmvAtOnce;
         return gmmk::launch_gmv(p, h->cu_count, static_cast<hipStream_t>(stream));

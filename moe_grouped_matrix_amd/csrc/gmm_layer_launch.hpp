@@ -53,7 +53,7 @@ struct GmvParams {
   int32_t T, k, n, G, N, K, nb, blk;
   int32_t fmt;  // 3 int4, 4 uint4, 5 fp4 e2m1
   int32_t scale_kind, ids64, w_f32, out_f32, per_slot;
-  int32_t experts;     // most experts that the slots can choose: min(n, G)
+  int32_t experts;     // workgroups' experts: the r-th of those chosen, r < experts, or (experts = G) every one
   uint32_t blk_magic;  // block b of 32 elements lies in scale block b * blk_magic >> 31
   int32_t at_once;     // the weighted sums are taken in one launch, without the workspace
 };

@@ -207,17 +207,27 @@ gmm_status gmm_adamw_run(gmm_handle* h, const gmm_adamw_item* items, int64_t cou
         p.b2 = (float)a->beta2;
         p.c2 = (float)(1 - a->beta2);
         p.eps = (float)a->eps;
+        const bool eight = a->state_dtype == GMM_F8E4M3FN;
+        const int per = elem_size(a->param_dtype) + elem_size(a->grad_dtype) + 2 * (eight ? 1 : 4);
+        long long bytes = 0;  // that the step reads
+        for (int64_t i = 0; i < count; ++i) bytes += items[i].n * per;
         const auto run = [&] {
-          return gmmk::launch_adamw(p, a->param_dtype == GMM_F32, a->grad_dtype == GMM_F32,
-                                    a->state_dtype == GMM_F8E4M3FN, h->cu_count, static_cast<hipStream_t>(stream));
+          return gmmk::launch_adamw(p, a->param_dtype == GMM_F32, a->grad_dtype == GMM_F32, eight,
+                                    bytes > gmmk::kAdamCached, static_cast<hipStream_t>(stream));
         };
         hipError_t e = hipSuccess;
         for (int64_t i = 0; i < count; ++i) {
           const gmm_adamw_item& t = items[i];
           if (t.n == 0) continue;
+          const long long chunks = (t.n + gmmk::kAdamChunk - 1) / gmmk::kAdamChunk;
+          // (a launch numbers its chunks in 31 bits)
+          if (p.count && p.first[p.count] + chunks > (1ll << 30)) {
+            if ((e = run()) != hipSuccess) return e;
+            p.count = 0;
+          }
           p.item[p.count] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale,
                              static_cast<uint16_t*>(t.copy), t.n};
-          p.first[p.count + 1] = p.first[p.count] + (int32_t)((t.n + gmmk::kAdamChunk - 1) / gmmk::kAdamChunk);
+          p.first[p.count + 1] = p.first[p.count] + (int32_t)chunks;
           if (++p.count == gmmk::kAdamItems) {
             if ((e = run()) != hipSuccess) return e;
             p.count = 0;

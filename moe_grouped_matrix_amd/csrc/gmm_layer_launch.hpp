@@ -67,7 +67,8 @@ hipError_t launch_gmv(const GmvParams& p, int cu_count, hipStream_t stream);
 // AdamW: up to kAdamItems tensors a launch, cut into chunks.
 constexpr int kAdamItems = 48;
 constexpr int kAdamBlock = 256;   // elements that share a scale
-constexpr int kAdamChunk = 4096;  // elements that a workgroup takes at a time
+constexpr int kAdamChunk = 2048;  // elements of a workgroup
+constexpr long long kAdamCached = 96 << 20;  // a step that reads more streams past the caches
 struct AdamItem {
   void* p;
   const void* g;
@@ -93,7 +94,7 @@ struct AdamParams {
   const float* grad_scale;
 };
 static_assert(sizeof(AdamParams) <= 4096, "kernel arguments");
-hipError_t launch_adamw(const AdamParams& p, bool p_f32, bool g_f32, bool eight, int cu_count, hipStream_t stream);
+hipError_t launch_adamw(const AdamParams& p, bool p_f32, bool g_f32, bool eight, bool stream_loads, hipStream_t stream);
 
 struct AdamFactors {
   float decay, rate, root_scale;

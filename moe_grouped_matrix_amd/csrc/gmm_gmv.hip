@@ -37,13 +37,22 @@ namespace gmmk {
 
 namespace {
 
-constexpr int kMaxSlots = 4096;
+constexpr int kWaves = 4;  // of a workgroup
+constexpr int kDepth = 2;  // chunks of a wave in flight
 
-__device__ __forceinline__ int slot_expert(const GmvParams& p, int i) {
-  if (!p.ids) return 0;
-  const long long id = p.ids64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
-  return id >= 0 && id < p.G ? (int)id : -1;
+// The id of a slot, as it was loaded (a 64-bit one in two halves), and the
+// expert that it names, -1 for none.
+struct SlotId {
+  unsigned lo, hi;
+};
+__device__ __forceinline__ SlotId load_id(const GmvParams& p, int i) {
+  const unsigned* const w = static_cast<const unsigned*>(p.ids) + ((long long)i << p.ids64);
+  return {w[0], w[p.ids64]};
 }
+__device__ __forceinline__ int expert_of(const GmvParams& p, SlotId id) {
+  return id.lo < (unsigned)p.G && (!p.ids64 || id.hi == 0) ? (int)id.lo : -1;
+}
+__device__ __forceinline__ int slot_expert(const GmvParams& p, int i) { return p.ids ? expert_of(p, load_id(p, i)) : 0; }
 __device__ __forceinline__ float slot_weight(const GmvParams& p, int i) {
   return p.w_f32 ? static_cast<const float*>(p.weights)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(p.weights)[i]);
 }
@@ -57,16 +66,26 @@ __device__ __forceinline__ void store_out(const GmvParams& p, long long o, float
 
 // How codes become operands, and how scales meet them.
 enum Kind : int {
-  kInt,    // int4, uint4: scale and zero point per block of a multiple of 32
-  kFp4,    // fp4 with f32 or bf16 scales
+  kInt,    // int4, uint4: a scale per block of a multiple of 32
+  kZero,   // the same with zero points
+  kFp4,    // fp4 with such scales
   kMicro,  // fp4 with E8M0 scales of blocks of 32
 };
+constexpr bool integer(Kind k) { return k == kInt || k == kZero; }
+
+// A scale or zero point as it was loaded: f32 bits, bf16 bits, or an E8M0 byte.
+// What is loaded is left alone until it is used, and types are the kernel's, not
+// the loads', so that no load waits for another.
+template <class S>
+__device__ __forceinline__ int as_f32(int bits) {
+  return sizeof(S) == 2 ? bits << 16 : bits;
+}
 
 // Eight codes as bf16, in the order of ordered_x.
 template <Kind KIND>
 __device__ __forceinline__ bf16x8 widen8(unsigned w, int byte) {
   i32x4 r;
-  if constexpr (KIND == kInt) {
+  if constexpr (integer(KIND)) {
     const unsigned even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
     r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.f, false));
     r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.f, true));
@@ -82,7 +101,7 @@ __device__ __forceinline__ bf16x8 widen8(unsigned w, int byte) {
 // 1 3 5 7 for int4 and uint4.
 template <Kind KIND>
 __device__ __forceinline__ bf16x8 ordered_x(i32x4 x) {
-  if constexpr (KIND != kInt) return __builtin_bit_cast(bf16x8, x);
+  if constexpr (!integer(KIND)) return __builtin_bit_cast(bf16x8, x);
   const i32x4 r{(int)__builtin_amdgcn_perm(x[1], x[0], 0x05040100), (int)__builtin_amdgcn_perm(x[3], x[2], 0x05040100),
                 (int)__builtin_amdgcn_perm(x[1], x[0], 0x07060302), (int)__builtin_amdgcn_perm(x[3], x[2], 0x07060302)};
   return __builtin_bit_cast(bf16x8, r);
@@ -118,162 +137,150 @@ __device__ __forceinline__ i32x4 spread4(int v) {
   return i32x4{a, b, c, e};
 }
 
-// One chunk of 128 elements of K: the lane's codes of NT column tiles, its
-// scales and zero points (of its own block of 32), and its x elements of the
-// four blocks (FEW: of one of them).
-template <int NT, bool FEW>
-struct Chunk {
-  i32x4 w[NT];
-  int s[NT], z[NT];
+// A lane's share of one chunk of 128 elements of K of its column: the codes of
+// its own block of 32, and that block's scale and zero point.
+struct Weights {
+  i32x4 w;
+  int s, z;
+};
+
+// Where a wave reads one expert's column: the lane's row of codes, and the index
+// of its column's first scale.
+struct Column {
+  const uint8_t* w;
+  long long scale;
+};
+
+__device__ __forceinline__ Column column_of(const GmvParams& p, int expert, int col) {
+  const int c = col < p.N ? col : p.N - 1;  // (past the last: read, and not stored)
+  return {p.rhs + ((long long)expert * p.N + c) * (p.K / 2), (long long)expert * p.nb * p.N + c};
+}
+
+template <Kind KIND, class S>
+__device__ __forceinline__ void load_weights(Weights& d, const GmvParams& p, const Column& src, int c, int q) {
+  const int k0 = 128 * c, mine = k0 + 32 * q < p.K ? k0 + 32 * q : k0;  // (past K: read elsewhere, and not used)
+  d.w = *reinterpret_cast<const i32x4*>(src.w + mine / 2);
+  const int b = KIND == kMicro ? mine >> 5 : (int)(((unsigned long long)((unsigned)mine >> 5) * p.blk_magic) >> 31);
+  const long long i = src.scale + (long long)b * p.N;
+  d.s = static_cast<int>(static_cast<const S*>(p.scale)[i]);
+  if constexpr (KIND == kZero) d.z = static_cast<int>(static_cast<const S*>(p.zero)[i]);
+}
+
+// The x operands of one chunk: of its four blocks, or (FEW) of all at once.
+template <bool FEW>
+struct Rows {
   i32x4 x[FEW ? 1 : 4];
 };
 
-// What a wave reads for one expert.
-template <int NT>
-struct Source {
-  const uint8_t* w;   // the expert's codes
-  long long scale;    // index of its first scale
-  long long row[NT];  // the lane's columns: offset of the codes
-  int col[NT];        // and the columns
-  const uint16_t* x;  // the lane's row of x
-};
-
-template <Kind KIND, int NT, bool FEW>
-__device__ __forceinline__ void load_chunk(Chunk<NT, FEW>& d, const GmvParams& p, const Source<NT>& src, int c, int q) {
-  const int k0 = 128 * c, mine = k0 + 32 * q < p.K ? k0 + 32 * q : k0;  // (past K: read elsewhere, and not used)
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-    d.w[t] = *reinterpret_cast<const i32x4*>(src.w + src.row[t] + mine / 2);
-  const int b = KIND == kMicro ? mine >> 5 : (int)(((unsigned long long)((unsigned)mine >> 5) * p.blk_magic) >> 31);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const long long i = src.scale + (long long)b * p.N + src.col[t];
-    if constexpr (KIND == kMicro) {
-      d.s[t] = static_cast<const uint8_t*>(p.scale)[i];
-    } else if (p.scale_kind == kGmvF32) {
-      d.s[t] = static_cast<const int*>(p.scale)[i];
-    } else {
-      d.s[t] = static_cast<const uint16_t*>(p.scale)[i] << 16;
-    }
-    if constexpr (KIND == kInt)
-      if (p.zero)
-        d.z[t] = p.scale_kind == kGmvF32 ? static_cast<const int*>(p.zero)[i] : static_cast<const uint16_t*>(p.zero)[i] << 16;
-  }
+template <bool FEW>
+__device__ __forceinline__ void load_rows(Rows<FEW>& d, const GmvParams& p, const uint16_t* x, int c, int q) {
+  const int k0 = 128 * c;
   if constexpr (FEW) {
     const int i = threadIdx.x & 3, k = k0 + 32 * i < p.K ? k0 + 32 * i : k0;
-    d.x[0] = *reinterpret_cast<const i32x4*>(src.x + k + 8 * q);
+    d.x[0] = *reinterpret_cast<const i32x4*>(x + k + 8 * q);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int k = k0 + 32 * i < p.K ? k0 + 32 * i : k0;
-      d.x[i] = *reinterpret_cast<const i32x4*>(src.x + k + 8 * q);
+      d.x[i] = *reinterpret_cast<const i32x4*>(x + k + 8 * q);
     }
   }
 }
 
-// The wave's sums: tot[t][r] of lane (q, n) for column n of tile t and row q
-// (FEW) or 4 q + r.  fp4 with E8M0 scales needs no folds, and sums in the matrix
+__device__ __forceinline__ bf16x8 ones() {
+  const i32x4 one4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
+  return __builtin_bit_cast(bf16x8, one4);
+}
+
+// The wave's sums: tot[r] of lane (q, n) for column n of the tile and row q (FEW)
+// or 4 q + r.  fp4 with E8M0 scales needs no folds, and sums in the matrix
 // cores' results, run (FEW: one for each block of a chunk).
-template <int NT, bool FEW>
+template <bool FEW>
 struct Sums {
-  float tot[NT][FEW ? 1 : 4];
-  f32x4 run[NT][FEW ? 4 : 1];
+  float tot[FEW ? 1 : 4];
+  f32x4 run[FEW ? 4 : 1];
 };
 
-template <int NT, bool FEW>
-__device__ __forceinline__ void clear(Sums<NT, FEW>& a) {
+template <bool FEW>
+__device__ __forceinline__ void clear(Sums<FEW>& a) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (float& v : a.tot) v = 0.f;
 #pragma unroll
-    for (float& v : a.tot[t]) v = 0.f;
-#pragma unroll
-    for (f32x4& v : a.run[t]) v = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (f32x4& v : a.run) v = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// Adds the products of chunk c.  WHOLE: its four blocks share their scale (scale
-// blocks are multiples of 128).  WEIGHTED: times `weight`.
-template <Kind KIND, bool WHOLE, bool WEIGHTED, int NT, bool FEW>
-__device__ __forceinline__ void use_chunk(Sums<NT, FEW>& a, Chunk<NT, FEW>& d, const GmvParams& p, int c, float weight) {
+// Adds the products of chunk c, the rows being in order (ordered_x).  WHOLE: its
+// four blocks share their scale (scale blocks are multiples of 128).  WEIGHTED:
+// times `weight`.
+template <Kind KIND, class S, bool WHOLE, bool WEIGHTED, bool FEW>
+__device__ __forceinline__ void use_chunk(Sums<FEW>& a, Weights d, const Rows<FEW>& rows, const GmvParams& p, int c,
+                                          float weight) {
   const int left = (p.K >> 5) - 4 * c;  // blocks from here on
   const f32x4 none{0.f, 0.f, 0.f, 0.f};
-  const i32x4 one4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
-  const float base = KIND == kInt && p.fmt == 3 ? 8.f : 0.f;
-  const int flip = KIND == kInt && p.fmt == 3 ? (int)0x88888888u : 0;
-  constexpr bool CHAIN = KIND == kMicro && !WEIGHTED;
-  constexpr int ROWS = FEW ? 1 : 4;
-  i32x4 s4[NT], z4[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if constexpr (KIND == kInt) d.w[t] ^= flip;
-    transpose4(d.w[t]);
-    if constexpr (KIND == kMicro || !WHOLE) {
-      s4[t] = spread4(d.s[t]);
-      if constexpr (KIND == kInt)
-        if (p.zero) z4[t] = spread4(d.z[t]);
-    }
+  const bool int4 = integer(KIND) && p.fmt == 3;
+  const float base = int4 ? 8.f : 0.f;
+  constexpr bool CHAIN = KIND == kMicro && !WEIGHTED, TOGETHER = WHOLE || KIND == kMicro;
+  i32x4 s4, z4;
+  if constexpr (integer(KIND)) d.w ^= int4 ? (int)0x88888888u : 0;
+  transpose4(d.w);
+  if constexpr (KIND == kMicro || !WHOLE) {
+    s4 = spread4(d.s);
+    if constexpr (KIND == kZero) z4 = spread4(d.z);
   }
   // sums of products `got` and of x `sum`, for row r
-  auto fold = [&](int t, int r, float got, float sum, int scale, int zero) __attribute__((always_inline)) {
-    float s = KIND == kMicro ? 1.f : __int_as_float(scale);
+  auto fold = [&](int r, float got, float sum, int scale, int zero) __attribute__((always_inline)) {
+    float s = KIND == kMicro ? 1.f : __int_as_float(as_f32<S>(scale));
     if constexpr (WEIGHTED) s *= weight;
-    if constexpr (KIND == kInt) got = __builtin_fmaf(-(p.zero ? __int_as_float(zero) + base : base), sum, got);
-    a.tot[t][r] = __builtin_fmaf(s, got, a.tot[t][r]);
+    if constexpr (integer(KIND))
+      got = __builtin_fmaf(-(KIND == kZero ? __int_as_float(as_f32<S>(zero)) + base : base), sum, got);
+    a.tot[r] = __builtin_fmaf(s, got, a.tot[r]);
   };
-  f32x4 acc[NT], sum = none;
-  float few[NT], few_sum = 0.f;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    acc[t] = none;
-    few[t] = 0.f;
-  }
-  bf16x8 x = ordered_x<KIND>(d.x[0]);
-  if constexpr (FEW && KIND == kInt) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, none, 0, 0, 0);
+  f32x4 acc = none, sum = none;
+  float few = 0.f, few_sum = 0.f;
+  bf16x8 x = __builtin_bit_cast(bf16x8, rows.x[0]);
+  if constexpr (FEW && integer(KIND)) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones(), none, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (i >= left) break;
     if constexpr (!FEW) {
-      if (i > 0) x = ordered_x<KIND>(d.x[i]);
-      if constexpr (KIND == kInt) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, WHOLE ? sum : none, 0, 0, 0);
+      if (i > 0) x = __builtin_bit_cast(bf16x8, rows.x[i]);
+      if constexpr (integer(KIND)) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones(), WHOLE ? sum : none, 0, 0, 0);
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const bf16x8 w = widen8<KIND>((unsigned)d.w[t][i], KIND == kMicro ? s4[t][i] : 0);
-      if constexpr (CHAIN) {
-        f32x4& run = a.run[t][FEW ? i : 0];
-        run = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, run, 0, 0, 0);
-        continue;
-      }
-      constexpr bool TOGETHER = WHOLE || KIND == kMicro;
-      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, TOGETHER && !FEW ? acc[t] : none, 0, 0, 0);
-      if constexpr (!TOGETHER) {
-        if constexpr (FEW) {
-          fold(t, 0, acc[t][i], sum[i], s4[t][i], z4[t][i]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) fold(t, r, acc[t][r], sum[r], s4[t][i], z4[t][i]);
-        }
-      } else if constexpr (FEW) {
-        few[t] += acc[t][i];
-      }
+    const bf16x8 w = widen8<KIND>((unsigned)d.w[i], KIND == kMicro ? s4[i] : 0);
+    if constexpr (CHAIN) {
+      f32x4& run = a.run[FEW ? i : 0];
+      run = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, run, 0, 0, 0);
+      continue;
     }
-    if constexpr (FEW && WHOLE) few_sum += sum[i];
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, TOGETHER && !FEW ? acc : none, 0, 0, 0);
+    if constexpr (!TOGETHER) {
+      if constexpr (FEW) {
+        fold(0, acc[i], sum[i], s4[i], z4[i]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) fold(r, acc[r], sum[r], s4[i], z4[i]);
+      }
+    } else if constexpr (FEW) {
+      few += acc[i];
+      few_sum += sum[i];
+    }
   }
-  if constexpr (!CHAIN && (WHOLE || KIND == kMicro)) {
+  if constexpr (!CHAIN && TOGETHER) {
+    if constexpr (FEW) {
+      fold(0, few, few_sum, d.s, d.z);
+    } else {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) fold(t, r, FEW ? few[t] : acc[t][r], FEW ? few_sum : sum[r], d.s[t], d.z[t]);
+      for (int r = 0; r < 4; ++r) fold(r, acc[r], sum[r], d.s, d.z);
+    }
   }
 }
 
 // What the sums came to.
-template <Kind KIND, bool WEIGHTED, int NT, bool FEW>
-__device__ __forceinline__ float total(const Sums<NT, FEW>& a, int t, int r) {
-  if constexpr (KIND != kMicro || WEIGHTED) return a.tot[t][r];
-  if constexpr (FEW) return (a.run[t][0][0] + a.run[t][1][1]) + (a.run[t][2][2] + a.run[t][3][3]);
-  return a.run[t][0][r];
+template <Kind KIND, bool WEIGHTED, bool FEW>
+__device__ __forceinline__ float total(const Sums<FEW>& a, int r) {
+  if constexpr (KIND != kMicro || WEIGHTED) return a.tot[r];
+  if constexpr (FEW) return (a.run[0][0] + a.run[1][1]) + (a.run[2][2] + a.run[3][3]);
+  return a.run[0][r];
 }
 
 // The slots of the r-th expert that any slot chose: into list; returns how
@@ -284,6 +291,13 @@ __device__ __forceinline__ float total(const Sums<NT, FEW>& a, int t, int r) {
 struct Found {
   int expert, count;
 };
+
+// (without ids every slot has expert 0)
+__device__ __forceinline__ Found find_all(const GmvParams& p, uint16_t* list) {
+  for (int i = threadIdx.x & 63; i < p.n; i += 64) list[i] = (uint16_t)i;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return {0, p.n};
+}
 
 __device__ __forceinline__ Found find_few(const GmvParams& p, int r, uint16_t* list) {
   const int lane = threadIdx.x & 63;
@@ -315,16 +329,18 @@ __device__ __forceinline__ Found find_slots(const GmvParams& p, int g, uint16_t*
   const unsigned long long below = (1ull << lane) - 1;
   int count = 0;
   for (int i0 = 0; i0 < p.n; i0 += 512) {
-    int id[8];
+    SlotId id[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int i = i0 + 64 * u + lane;
-      id[u] = i < p.n ? slot_expert(p, i) : -1;
+      id[u] = load_id(p, i < p.n ? i : p.n - 1);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const unsigned long long mine = __ballot(id[u] == g);
-      if (id[u] == g) list[count + __builtin_popcountll(mine & below)] = (uint16_t)(i0 + 64 * u + lane);
+      const int i = i0 + 64 * u + lane;
+      const bool hit = i < p.n && expert_of(p, id[u]) == g;
+      const unsigned long long mine = __ballot(hit);
+      if (hit) list[count + __builtin_popcountll(mine & below)] = (uint16_t)i;
       count += __builtin_popcountll(mine);
     }
   }
@@ -332,12 +348,11 @@ __device__ __forceinline__ Found find_slots(const GmvParams& p, int g, uint16_t*
   return {count ? g : -1, count};
 }
 
-template <int T>
 __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* list) {
-  __shared__ int chosen[kMaxGroups];
-  __shared__ int wave_tot[T / 64];
+  __shared__ uint8_t chosen[kMaxGroups];
+  __shared__ int wave_tot[16];
   __shared__ int expert, count;
-  constexpr int PER = kMaxGroups / T;
+  constexpr int T = 64 * kWaves, per = kMaxGroups / T;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   for (int g = tid; g < kMaxGroups; g += T) chosen[g] = 0;
   if (tid == 0) {
@@ -351,8 +366,8 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
   }
   __syncthreads();
   int mine = 0;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) mine += chosen[tid * PER + j];
+  for (int j = 0; j < per; ++j)
+    mine += chosen[tid * per + j];
   int incl = mine;
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) {
@@ -364,7 +379,7 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
   int at = incl - mine;
   for (int i = 0; i < w; ++i) at += wave_tot[i];
   if (at <= r && r < at + mine) {
-    int g = tid * PER;
+    int g = tid * per;
     for (int left = r - at;; ++g)
       if (chosen[g] && left-- == 0) break;
     expert = g;
@@ -378,91 +393,101 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
   return {g, count};
 }
 
-template <int NT>
-__device__ __forceinline__ void set_columns(Source<NT>& src, const GmvParams& p, int n0, int n) {
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int col = n0 + 16 * t + n;
-    src.col[t] = col < p.N ? col : p.N - 1;  // (past the last: read, and not stored)
-    src.row[t] = (long long)src.col[t] * (p.K / 2);
-  }
-}
-
-// One pass over the expert's columns for rows list[first ..].
-template <Kind KIND, bool WHOLE, int NT, bool FEW, int W>
-__device__ __forceinline__ void pass(const GmvParams& p, Source<NT>& src, const uint16_t* list, int first, int rows, int n0,
-                                     float* join) {
-  constexpr int D = NT == 1 ? 3 : 2;  // chunks in flight
-  constexpr int ROWS = FEW ? 4 : 16;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, n = lane & 15;
-  const int row = FEW ? n >> 2 : n;
-  const int slot = list[first + (row < rows ? row : 0)];
-  src.x = p.x + (long long)(p.per_slot ? slot : slot / p.k) * p.K;
-  const int chunks = (p.K + 127) >> 7, lo = chunks * w / W, hi = chunks * (w + 1) / W;
-  Sums<NT, FEW> sums;
-  clear(sums);
-  Chunk<NT, FEW> d[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i)
-    if (lo + i < hi) load_chunk<KIND>(d[i], p, src, lo + i, q);
-  for (int c = lo; c < hi; c += D) {
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-      if (c + i < hi) {
-        use_chunk<KIND, WHOLE, false>(sums, d[i], p, c + i, 1.f);
-        if (c + i + D < hi) load_chunk<KIND>(d[i], p, src, c + i + D, q);
-      }
-  }
-  // join[wave][row][column]
+// The join: every wave's sums go to LDS, join[wave][row][column], and all threads
+// add them up, in the waves' order, and store.
+template <Kind KIND, bool FEW, int NT>
+__device__ __forceinline__ void join_tiles(const GmvParams& p, const Sums<FEW> (&sums)[NT], float* join, const uint16_t* list,
+                                           int rows, int n0) {
+  constexpr int ROWS = FEW ? 4 : 16, COLS = 16 * NT;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < ROWS / 4; ++r)
-      join[(w * ROWS + (FEW ? q : 4 * q + r)) * (16 * NT) + 16 * t + n] = total<KIND, false>(sums, t, r);
+      join[(w * ROWS + (FEW ? q : 4 * q + r)) * COLS + 16 * t + n] = total<KIND, false>(sums[t], r);
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * 16 * NT; i += 64 * W) {
-    const int rr = i / (16 * NT), col = i % (16 * NT);
-    if (n0 + col < p.N) {
-      float v = 0.f;
+  for (int i = threadIdx.x; i < rows * COLS; i += 64 * kWaves) {
+    const int col = n0 + i % COLS;
+    float v = 0.f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) v += join[(j * ROWS + rr) * (16 * NT) + col];
-      const long long o = (long long)list[first + rr] * p.N + n0 + col;
+    for (int j = 0; j < kWaves; ++j) v += join[j * ROWS * COLS + i];
+    if (col < p.N) {
+      const long long o = (long long)list[i / COLS] * p.N + col;
       if (p.weights)
         p.work[o] = v;
       else
         store_out(p, o, v);
     }
   }
-  __syncthreads();
 }
 
-template <Kind KIND, bool WHOLE, int NT>
-__global__ __launch_bounds__(256, 4) void gmv_kernel(GmvParams p) {
-  constexpr int W = 4;
-  __shared__ uint16_t list[kMaxSlots];
-  __shared__ float join[W * 16 * 16 * NT];
-  const int n0 = blockIdx.x * 16 * NT, n = threadIdx.x & 15;
+// One pass over the workgroup's columns, NT tiles of 16, for the rows of list (up
+// to four: FEW, or 16).  The waves share out K in contiguous runs of chunks; a wave
+// has D chunks of codes, scales and x in flight.
+template <Kind KIND, class S, bool WHOLE, bool FEW, int NT>
+__device__ __forceinline__ void pass(const GmvParams& p, int expert, const uint16_t* list, int rows, int n0, float* join) {
+  constexpr int D = kDepth;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, n = lane & 15;
+  const int chunks = (p.K + 127) >> 7, lo = chunks * w / kWaves, hi = chunks * (w + 1) / kWaves;
+  Column src[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) src[t] = column_of(p, expert, n0 + 16 * t + n);
+  const int row = FEW ? n >> 2 : n;
+  const int slot = list[row < rows ? row : 0];
+  const uint16_t* const x = p.x + (long long)(p.per_slot ? slot : slot / p.k) * p.K;
+  Weights d[D][NT];
+  Rows<FEW> xs[D];
+  auto load = [&](int i, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) load_weights<KIND, S>(d[i][t], p, src[t], c, q);
+    load_rows(xs[i], p, x, c, q);
+  };
+  Sums<FEW> sums[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) clear(sums[t]);
+  const int last = hi - 1;
+  if (lo < hi) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) load(i, lo + i < hi ? lo + i : last);
+    for (int c = lo; c < hi; c += D) {
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if (c + i < hi) {
+          for (i32x4& v : xs[i].x) v = __builtin_bit_cast(i32x4, ordered_x<KIND>(v));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) use_chunk<KIND, S, WHOLE, false>(sums[t], d[i][t], xs[i], p, c + i, 1.f);
+          if (c + i + D < hi) load(i, c + i + D);
+        }
+    }
+  }
+  join_tiles<KIND, FEW, NT>(p, sums, join, list, rows, n0);
+}
+
+template <Kind KIND, class S, bool WHOLE, int NT>
+__global__ __launch_bounds__(64 * kWaves, 4) void gmv_kernel(GmvParams p) {
+  __shared__ float join[kWaves * 16 * 16 * NT];
+  extern __shared__ uint16_t list[];  // [n]
+  const int n0 = blockIdx.x * 16 * NT;
   if ((int)blockIdx.y == p.experts) {  // slots without an expert: zeros
-    for (int i = threadIdx.x / (16 * NT); i < p.n; i += 256 / (16 * NT)) {
+    for (int i = threadIdx.x / (16 * NT); i < p.n; i += 64 * kWaves / (16 * NT)) {
       const int col = n0 + threadIdx.x % (16 * NT);
       if (col < p.N && slot_expert(p, i) < 0) store_out(p, (long long)i * p.N + col, 0.f);
     }
     return;
   }
-  const Found f = p.n <= 64 ? find_few(p, blockIdx.y, list)
+  const Found f = !p.ids ? find_all(p, list)
+                  : p.n <= 64 ? find_few(p, blockIdx.y, list)
                   : p.experts == p.G ? find_slots(p, blockIdx.y, list)
-                                     : find_many<64 * W>(p, blockIdx.y, list);
+                                     : find_many(p, blockIdx.y, list);
   if (f.expert < 0) return;
-  Source<NT> src;
-  set_columns(src, p, n0, n);
-  src.w = p.rhs + (long long)f.expert * p.N * (p.K / 2);
-  src.scale = (long long)f.expert * p.nb * p.N;
   for (int first = 0; first < f.count; first += 16) {
     const int rows = f.count - first < 16 ? f.count - first : 16;
+    if (first > 0) __syncthreads();  // (the join's buffer is free again)
     if (rows <= 4)
-      pass<KIND, WHOLE, NT, true, W>(p, src, list, first, rows, n0, join);
+      pass<KIND, S, WHOLE, true, NT>(p, f.expert, list + first, rows, n0, join);
     else
-      pass<KIND, WHOLE, NT, false, W>(p, src, list, first, rows, n0, join);
+      pass<KIND, S, WHOLE, false, NT>(p, f.expert, list + first, rows, n0, join);
   }
 }
 
@@ -470,7 +495,7 @@ __global__ __launch_bounds__(256, 4) void gmv_kernel(GmvParams p) {
 // of one token, its 16 waves share out the chunks of all its slots.  For a few
 // tokens, whose experts are mostly different ones, this saves the second
 // launch.
-template <Kind KIND, bool WHOLE>
+template <Kind KIND, class S, bool WHOLE>
 __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
   constexpr int W = 16;
   __shared__ int expert[64];
@@ -487,36 +512,34 @@ __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
     slot[at] = t * p.k + lane;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  Source<1> src;
-  set_columns(src, p, n0, n);
   const int chunks = (p.K + 127) >> 7, all = __builtin_popcountll(live) * chunks;
-  const int lo = all * w / W, hi = all * (w + 1) / W;
-  Sums<1, true> sums;
+  const int lo = (int)((long long)all * w / W), hi = (int)((long long)all * (w + 1) / W);
+  Sums<true> sums;
   clear(sums);
   constexpr int D = 3;
-  Chunk<1, true> d[D];
+  Weights d[D];
+  Rows<true> xs[D];
   float weight[D];
-  auto load = [&](Chunk<1, true>& into, float& wt, int item) __attribute__((always_inline)) {
-    const int j = item / chunks;
-    const int g = __builtin_amdgcn_readfirstlane(expert[j]), i = __builtin_amdgcn_readfirstlane(slot[j]);
-    src.w = p.rhs + (long long)g * p.N * (p.K / 2);
-    src.scale = (long long)g * p.nb * p.N;
-    src.x = p.x + (long long)(p.per_slot ? i : t) * p.K;
-    wt = slot_weight(p, i);
-    load_chunk<KIND>(into, p, src, item - j * chunks, q);
+  auto load = [&](int i, int item) __attribute__((always_inline)) {
+    const int j = item / chunks, c = item - j * chunks;
+    const int g = __builtin_amdgcn_readfirstlane(expert[j]), s = __builtin_amdgcn_readfirstlane(slot[j]);
+    weight[i] = slot_weight(p, s);
+    load_weights<KIND, S>(d[i], p, column_of(p, g, n0 + n), c, q);
+    load_rows(xs[i], p, p.x + (long long)(p.per_slot ? s : t) * p.K, c, q);
   };
 #pragma unroll
   for (int i = 0; i < D; ++i)
-    if (lo + i < hi) load(d[i], weight[i], lo + i);
+    if (lo + i < hi) load(i, lo + i);
   for (int c = lo; c < hi; c += D) {
 #pragma unroll
     for (int i = 0; i < D; ++i)
       if (c + i < hi) {
-        use_chunk<KIND, WHOLE, true>(sums, d[i], p, (c + i) % chunks, weight[i]);
-        if (c + i + D < hi) load(d[i], weight[i], c + i + D);
+        xs[i].x[0] = __builtin_bit_cast(i32x4, ordered_x<KIND>(xs[i].x[0]));
+        use_chunk<KIND, S, WHOLE, true>(sums, d[i], xs[i], p, (c + i) % chunks, weight[i]);
+        if (c + i + D < hi) load(i, c + i + D);
       }
   }
-  if (q == 0) join[w][n] = total<KIND, true>(sums, 0, 0);
+  if (q == 0) join[w][n] = total<KIND, true>(sums, 0);
   __syncthreads();
   if (threadIdx.x < 16 && n0 + n < p.N) {
     float v = 0.f;
@@ -539,28 +562,37 @@ __global__ __launch_bounds__(256) void gmv_join_kernel(GmvParams p) {
   store_out(p, (long long)t * p.N + n, sum);
 }
 
-template <Kind KIND, bool WHOLE>
+template <Kind KIND, class S, bool WHOLE>
 hipError_t launch(const GmvParams& p, int cu_count, hipStream_t s) {
+  const int all = (p.N + 15) / 16;
   if (p.at_once) {
-    hipLaunchKernelGGL((gmv_token_kernel<KIND, WHOLE>), dim3((p.N + 15) / 16, p.T), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((gmv_token_kernel<KIND, S, WHOLE>), dim3(all, p.T), dim3(1024), 0, s, p);
     return hipGetLastError();
   }
   const unsigned experts = p.experts + (p.weights ? 0 : 1);
+  const size_t lds = (size_t)p.n * 2;
   if ((long long)((p.N + 31) / 32) * p.experts >= 2 * cu_count)
-    hipLaunchKernelGGL((gmv_kernel<KIND, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(64 * kWaves), lds, s, p);
   else
-    hipLaunchKernelGGL((gmv_kernel<KIND, WHOLE, 1>), dim3((p.N + 15) / 16, experts), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 1>), dim3(all, experts), dim3(64 * kWaves), lds, s, p);
   if (p.weights) hipLaunchKernelGGL(gmv_join_kernel, dim3((p.N + 255) / 256, p.T), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
+template <Kind KIND>
+hipError_t by_scale(const GmvParams& p, int cu_count, hipStream_t s) {
+  const bool whole = p.blk % 128 == 0;
+  if (p.scale_kind == kGmvF32)
+    return whole ? launch<KIND, uint32_t, true>(p, cu_count, s) : launch<KIND, uint32_t, false>(p, cu_count, s);
+  return whole ? launch<KIND, uint16_t, true>(p, cu_count, s) : launch<KIND, uint16_t, false>(p, cu_count, s);
+}
+
 }  // namespace
 
-hipError_t launch_gmv(const GmvParams& p, int cu_count, hipStream_t stream) {
-  if (p.scale_kind == kGmvE8m0) return launch<kMicro, false>(p, cu_count, stream);
-  const bool whole = p.blk % 128 == 0;
-  if (p.fmt == 5) return whole ? launch<kFp4, true>(p, cu_count, stream) : launch<kFp4, false>(p, cu_count, stream);
-  return whole ? launch<kInt, true>(p, cu_count, stream) : launch<kInt, false>(p, cu_count, stream);
+hipError_t launch_gmv(const GmvParams& p, int cu_count, hipStream_t s) {
+  if (p.scale_kind == kGmvE8m0) return launch<kMicro, uint8_t, false>(p, cu_count, s);
+  if (p.fmt == 5) return by_scale<kFp4>(p, cu_count, s);
+  return p.zero ? by_scale<kZero>(p, cu_count, s) : by_scale<kInt>(p, cu_count, s);
 }
 
 }  // namespace gmmk

@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kWaves = 4;  // of a workgroup
 constexpr int kDepth = 2;  // chunks of a wave in flight
+constexpr int kManyX = 1;  // and of x with more than four rows
 
 // The id of a slot, as it was loaded (a 64-bit one in two halves), and the
 // expert that it names, -1 for none.
@@ -426,7 +427,7 @@ __device__ __forceinline__ void join_tiles(const GmvParams& p, const Sums<FEW> (
 // has D chunks of codes, scales and x in flight.
 template <Kind KIND, class S, bool WHOLE, bool FEW, int NT>
 __device__ __forceinline__ void pass(const GmvParams& p, int expert, const uint16_t* list, int rows, int n0, float* join) {
-  constexpr int D = kDepth;
+  constexpr int D = kDepth, DX = FEW ? kDepth : kManyX;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, n = lane & 15;
   const int chunks = (p.K + 127) >> 7, lo = chunks * w / kWaves, hi = chunks * (w + 1) / kWaves;
@@ -437,11 +438,10 @@ __device__ __forceinline__ void pass(const GmvParams& p, int expert, const uint1
   const int slot = list[row < rows ? row : 0];
   const uint16_t* const x = p.x + (long long)(p.per_slot ? slot : slot / p.k) * p.K;
   Weights d[D][NT];
-  Rows<FEW> xs[D];
+  Rows<FEW> xs[DX];
   auto load = [&](int i, int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) load_weights<KIND, S>(d[i][t], p, src[t], c, q);
-    load_rows(xs[i], p, x, c, q);
   };
   Sums<FEW> sums[NT];
 #pragma unroll
@@ -450,13 +450,17 @@ __device__ __forceinline__ void pass(const GmvParams& p, int expert, const uint1
   if (lo < hi) {
 #pragma unroll
     for (int i = 0; i < D; ++i) load(i, lo + i < hi ? lo + i : last);
+#pragma unroll
+    for (int i = 0; i < DX; ++i) load_rows(xs[i], p, x, lo + i < hi ? lo + i : last, q);
     for (int c = lo; c < hi; c += D) {
 #pragma unroll
       for (int i = 0; i < D; ++i)
         if (c + i < hi) {
-          for (i32x4& v : xs[i].x) v = __builtin_bit_cast(i32x4, ordered_x<KIND>(v));
+          Rows<FEW>& xi = xs[i % DX];
+          for (i32x4& v : xi.x) v = __builtin_bit_cast(i32x4, ordered_x<KIND>(v));
 #pragma unroll
-          for (int t = 0; t < NT; ++t) use_chunk<KIND, S, WHOLE, false>(sums[t], d[i][t], xs[i], p, c + i, 1.f);
+          for (int t = 0; t < NT; ++t) use_chunk<KIND, S, WHOLE, false>(sums[t], d[i][t], xi, p, c + i, 1.f);
+          if (c + i + DX < hi) load_rows(xi, p, x, c + i + DX, q);
           if (c + i + D < hi) load(i, c + i + D);
         }
     }
@@ -465,14 +469,19 @@ __device__ __forceinline__ void pass(const GmvParams& p, int expert, const uint1
 }
 
 template <Kind KIND, class S, bool WHOLE, int NT>
-__global__ __launch_bounds__(64 * kWaves, 4) void gmv_kernel(GmvParams p) {
+__global__ __launch_bounds__(64 * kWaves, 5) void gmv_kernel(GmvParams p) {
   __shared__ float join[kWaves * 16 * 16 * NT];
   extern __shared__ uint16_t list[];  // [n]
   const int n0 = blockIdx.x * 16 * NT;
   if ((int)blockIdx.y == p.experts) {  // slots without an expert: zeros
-    for (int i = threadIdx.x / (16 * NT); i < p.n; i += 64 * kWaves / (16 * NT)) {
-      const int col = n0 + threadIdx.x % (16 * NT);
-      if (col < p.N && slot_expert(p, i) < 0) store_out(p, (long long)i * p.N + col, 0.f);
+    const int lane = threadIdx.x & 63;
+    for (int i0 = 64 * (threadIdx.x >> 6); p.ids && i0 < p.n; i0 += 64 * kWaves) {
+      const SlotId id = load_id(p, i0 + lane < p.n ? i0 + lane : p.n - 1);
+      unsigned long long none = __ballot(i0 + lane < p.n && expert_of(p, id) < 0);
+      for (; none; none &= none - 1) {
+        const long long slot = i0 + __builtin_ctzll(none);
+        if (lane < 16 * NT && n0 + lane < p.N) store_out(p, slot * p.N + n0 + lane, 0.f);
+      }
     }
     return;
   }

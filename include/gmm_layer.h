@@ -52,6 +52,8 @@ extern "C" {
  *               others).  When read, an id outside [0,E) is no choice, and the
  *               same expert may appear twice in a token.
  *
+ * Scores below 2^-126 may count as 0.
+ *
  * A token counts when it is valid and has an expert that is not switched off.
  * A NaN or +inf logit of a token that counts makes what depends on it NaN.
  * Limits: 1 <= E <= 1024, 1 <= k <= 64, k <= E, T*E < 2^31 (GMM_E_UNSUPPORTED

@@ -83,9 +83,16 @@ __device__ __forceinline__ float exp_of(float x) {
   return __builtin_fmaf(e, left * 0x1.62e43p-1f, e);
 }
 
+// The logarithm of a sum of exponentials of which one is 1, and reciprocals: the
+// instructions' (1 ulp); no reciprocal of a sum of scores below 2^-126, which
+// counts as 0.
+__device__ __forceinline__ float log_of(float x) { return __builtin_amdgcn_logf(x) * 0x1.62e43p-1f; }
+__device__ __forceinline__ float over_of(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ float over_scores(float sum) { return sum >= 0x1p-126f ? over_of(sum) : 0.f; }
+
 // The sigmoids of z and of -z, each within a few u of itself.
 __device__ __forceinline__ void sigmoids(float z, float& s, float& not_s) {
-  const float e = exp_of(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
+  const float e = exp_of(-fabsf(z)), r = over_of(1.f + e), er = e * r;
   s = z >= 0.f ? r : er;
   not_s = z >= 0.f ? er : r;
 }
@@ -113,36 +120,43 @@ struct Row {
 
 // Asks for the logits; what is out of range is read elsewhere in the tensor
 // (which must have a token) and put right by row_state, so that the loads need
-// no branches.
-template <int L, int V>
+// no branches.  FULL: E is L V, and a lane's experts are a constant apart.
+template <int L, int V, bool FULL>
 __device__ __forceinline__ bool load_row(Row<V>& r, const RouterParams& p, long long t, int l) {
   const long long row = (t < p.T ? t : p.T - 1) * p.E;
   const int last = p.E - 1;
+  auto at = [&](int v) __attribute__((always_inline)) { return FULL || l + L * v < last ? l + L * v : last; };
   if (p.x_f32) {
     const float* const z = static_cast<const float*>(p.logits) + row;
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.z[v] = z[l + L * v < last ? l + L * v : last];
+    for (int v = 0; v < V; ++v) r.z[v] = z[at(v)];
   } else {
     const uint16_t* const z = static_cast<const uint16_t*>(p.logits) + row;
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.z[v] = bf16_bits_to_f32(z[l + L * v < last ? l + L * v : last]);
+    for (int v = 0; v < V; ++v) r.z[v] = bf16_bits_to_f32(z[at(v)]);
   }
   return t < p.T && (!p.valid || p.valid[t] != 0);
 }
 
-template <int L, int V>
+// What the row is.  (The logits of padding stay what they are: nothing that
+// comes of a token that does not count is kept.)
+template <int L, int V, bool FULL>
 __device__ __forceinline__ void row_state(Row<V>& r, const RouterParams& p, bool valid, int l) {
   float top = -kInf;
-  bool bad = false;
+  // a NaN or +inf is the largest of the bit patterns as signed numbers, or, with
+  // its sign set, as unsigned ones
+  int high = 0;
+  unsigned low = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    r.z[v] = valid && l + L * v < p.E ? r.z[v] : -kInf;
+    if constexpr (!FULL) r.z[v] = l + L * v < p.E ? r.z[v] : -kInf;
     top = fmaxf(top, r.z[v]);
-    bad |= !(r.z[v] < kInf);
+    high = max(high, __float_as_int(r.z[v]));
+    low = max(low, __float_as_uint(r.z[v]));
   }
   r.top = group_max<L>(top);
-  r.bad = group_any<L>(bad);
-  r.counts = r.bad || r.top > -kInf;
+  r.bad = group_any<L>(valid && (high >= 0x7F800000 || low > 0xFF800000u));
+  r.counts = valid && (r.bad || r.top > -kInf);
 }
 
 // ---------------------------------------------------------------------------
@@ -157,12 +171,14 @@ __device__ __forceinline__ void row_state(Row<V>& r, const RouterParams& p, bool
 // the lanes' lists alone, and the lane that held the best one moves its list
 // up.  More choices, and few values a lane, look at every value in every round.
 
+constexpr double kDead = -0x1p1000;  // of an expert that is switched off (its key has the id, too)
+
 __device__ __forceinline__ double choice_key(float value, int e) {
   const float x = value + 0.f;  // (-0 ranks as +0)
-  if (!(x > -kInf)) return -__builtin_inf();
-  const unsigned tag = x < 0.f ? (unsigned)e : 1023u - (unsigned)e;
-  return __longlong_as_double(__double_as_longlong((double)x) | tag);
+  const unsigned tag = ~((unsigned)(__float_as_int(x) >> 31) ^ (unsigned)e) & 1023u;
+  return __longlong_as_double(__double_as_longlong(__builtin_fmax((double)x, kDead)) | tag);
 }
+__device__ __forceinline__ bool alive(double key) { return key > 0.5 * kDead; }
 __device__ __forceinline__ int key_expert(double key) {
   const int tag = (int)(__double_as_longlong(key) & 1023);
   return key < 0 ? tag : 1023 - tag;
@@ -200,7 +216,7 @@ __device__ __forceinline__ void order8(double* k) {
   exchange(k[5], k[6]);
 }
 
-template <int L, int V, bool K8>
+template <int L, int V, bool K8, bool FULL>
 __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
   constexpr int R = 64 / L;
   const int l = threadIdx.x & (L - 1), r = (threadIdx.x & 63) / L, w = threadIdx.x >> 6;
@@ -208,14 +224,14 @@ __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
   for (long long t0 = (long long)blockIdx.x * (W * R); t0 < p.T; t0 += (long long)gridDim.x * (W * R)) {
     const long long t = t0 + w * R + r;
     Row<V> x;
-    const bool valid = load_row<L, V>(x, p, t, l);
-    row_state<L, V>(x, p, valid, l);
+    const bool valid = load_row<L, V, FULL>(x, p, t, l);
+    row_state<L, V, FULL>(x, p, valid, l);
     float over_sum = 0.f;  // of the softmax, relative to the largest logit
     if (!p.sigmoid && (p.bias || !p.renorm)) {
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) sum += exp_of(x.z[v] - x.top);
-      over_sum = 1.f / group_sum<L>(sum);
+      over_sum = over_of(group_sum<L>(sum));
     }
     double key[V];
     bool bad = x.bad;
@@ -226,7 +242,7 @@ __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
         float rank = x.z[v];
         if (rank > -kInf && e < p.E) {
           rank = (p.sigmoid ? sigmoid(rank) : exp_of(rank - x.top) * over_sum) + p.bias[e];
-          bad |= !(rank < kInf);
+          bad |= x.counts && !(rank < kInf);
         }
         key[v] = choice_key(rank, e);
       }
@@ -236,7 +252,7 @@ __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
       for (int v = 0; v < V; ++v) key[v] = choice_key(x.z[v], l + L * v);
     }
     // lane j keeps the j-th choice
-    double mine = -__builtin_inf();
+    double mine = kDead;
     if constexpr (K8) {
 #pragma unroll
       for (int i = 0; i < V; i += 8) order8(key + i);
@@ -264,11 +280,11 @@ __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
         for (int v = 1; v < V; ++v) best = __builtin_fmax(best, key[v]);
         best = group_max<L>(best);
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? -__builtin_inf() : key[v];
+        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? kDead : key[v];
         mine = l == j ? best : mine;
       }
     }
-    const bool there = mine > -__builtin_inf() && !bad;
+    const bool there = alive(mine) && x.counts && !bad;
     const int id = there ? key_expert(mine) : -1;
     float z = -kInf;
     if (!p.bias)
@@ -285,7 +301,7 @@ __global__ __launch_bounds__(kRouterT, 4) void route_kernel(RouterParams p) {
     }
     if (p.renorm) {
       const float total = group_sum<L>(s);
-      s = total > 0.f ? s / total : 0.f;
+      s *= over_scores(total);
     }
     if (t < p.T && l < p.k) {
       p.ids_out[t * p.k + l] = id;
@@ -324,7 +340,7 @@ __device__ __forceinline__ void finish_loss(const RouterParams& p, double P, lon
   }
 }
 
-template <int L, int V>
+template <int L, int V, bool FULL>
 __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams p) {
   constexpr int R = 64 / L, W = kBalanceT / 64;
   __shared__ int hist[kMaxGroups];
@@ -344,19 +360,19 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
   const long long end = p.T + w * R + r;
   Row<V> next;
   bool next_valid = false;
-  if (p.T > 0) next_valid = load_row<L, V>(next, p, t, l);  // (there may be no token at all)
+  if (p.T > 0) next_valid = load_row<L, V, FULL>(next, p, t, l);  // (there may be no token at all)
   long long id = load_id(p, t, l);
   for (; t < end; t += step) {
     Row<V> x = next;
     const bool valid = next_valid;
-    if (t + step < end) next_valid = load_row<L, V>(next, p, t + step, l);
+    if (t + step < end) next_valid = load_row<L, V, FULL>(next, p, t + step, l);
     if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
     for (int j = l + L; j < p.k; j += L) {
       id = load_id(p, t, j);
       if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
     }
     id = load_id(p, t + step, l);
-    row_state<L, V>(x, p, valid, l);
+    row_state<L, V, FULL>(x, p, valid, l);
     float e[V], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -364,7 +380,7 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
       sum += e[v];
     }
     sum = group_sum<L>(sum);
-    const float lse = x.bad ? kNan : x.top + logf(sum);
+    const float lse = x.bad ? kNan : x.top + log_of(sum);
     if (p.sigmoid) {
       sum = 0.f;
 #pragma unroll
@@ -375,7 +391,7 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
       sum = group_sum<L>(sum);
     }
     if (x.counts) {
-      const float over = x.bad ? kNan : sum > 0.f ? 1.f / sum : 0.f;
+      const float over = x.bad ? kNan : over_scores(sum);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = __builtin_fmaf(e[v], over, acc[v]);
       z2 = __builtin_fmaf(lse, lse, z2);
@@ -492,7 +508,7 @@ __global__ __launch_bounds__(kBalanceT) void balance_final_kernel(RouterParams p
 //                  not renormalised (the sum is 0 there); sigmoid: + u_j (1 - s_j)
 // The u_j go to their experts' lanes through a row of LDS a group.
 
-template <int L, int V, bool SIGMOID>
+template <int L, int V, bool SIGMOID, bool FULL>
 __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
   constexpr int R = 64 / L, W = kRouterT / 64;
   __shared__ float picked[W * R][L * V];
@@ -505,7 +521,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
   // A token's logits, and lane j's slot j; the next token's are asked for
   // before the present one is worked on.
   Row<V> next;
-  bool next_valid = load_row<L, V>(next, p, t, l);
+  bool next_valid = load_row<L, V, FULL>(next, p, t, l);
   long long next_id = -1;
   float next_g = 0.f;
   auto load_slot = [&](long long t1) __attribute__((always_inline)) {
@@ -543,10 +559,10 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
     const int id = (int)next_id;
     float g = next_g;
     if (t + step < end) {
-      next_valid = load_row<L, V>(next, p, t + step, l);
+      next_valid = load_row<L, V, FULL>(next, p, t + step, l);
       if (p.dweights) load_slot(t + step);
     }
-    row_state<L, V>(x, p, valid, l);
+    row_state<L, V, FULL>(x, p, valid, l);
     float z = -kInf;
     if (p.dweights) {  // the chosen logits, from their lanes
 #pragma unroll
@@ -564,7 +580,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
       sum += soft[v];
     }
     sum = group_sum<L>(sum);
-    const float over_sum = 1.f / sum, lse = x.top + logf(sum);
+    const float over_sum = over_of(sum), lse = x.top + log_of(sum);
     float over = over_sum;  // of the sum of the scores that soft or s hold
     if constexpr (SIGMOID) {
       float ssum = 0.f;
@@ -575,7 +591,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
         about = __builtin_fmaf(a[v], s[v], about);
       }
       ssum = group_sum<L>(ssum);
-      over = ssum > 0.f ? 1.f / ssum : 0.f;
+      over = over_scores(ssum);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) about = __builtin_fmaf(a[v], soft[v], about);
@@ -597,7 +613,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
       }
       if (p.renorm) {
         const float total = group_sum<L>(q);
-        q = total > 0.f ? q / total : 0.f;
+        q *= over_scores(total);
         g -= group_sum<L>(q * g);
       }
       float u = p.scale * q * g;
@@ -636,20 +652,23 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
       else
         d[v] = soft[v] * over_sum * (a[v] - about - off + c);
       if (p.dweights) d[v] += mine[l + L * v];
-      if (x.bad) d[v] = kNan;
-      if (!x.counts || x.z[v] == -kInf) d[v] = 0.f;
+      if (x.z[v] == -kInf) d[v] = 0.f;
+    }
+    if (__ballot(x.bad || !x.counts) != 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = x.bad ? kNan : x.counts ? d[v] : 0.f;
     }
     if (t < p.T) {
       if (p.x_f32) {
         float* const out = static_cast<float*>(p.dlogits) + t * p.E;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (l + L * v < p.E) out[l + L * v] = d[v];
+          if (FULL || l + L * v < p.E) out[l + L * v] = d[v];
       } else {
         uint16_t* const out = static_cast<uint16_t*>(p.dlogits) + t * p.E;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (l + L * v < p.E) out[l + L * v] = f32_to_bf16_rne(d[v]);
+          if (FULL || l + L * v < p.E) out[l + L * v] = f32_to_bf16_rne(d[v]);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -665,21 +684,33 @@ int row_grid(const RouterParams& p, int L, int cu_count, int per_cu) {
 
 template <int L, int V, bool K8>
 hipError_t route(const RouterParams& p, int cus, hipStream_t s) {
-  hipLaunchKernelGGL((route_kernel<L, V, K8>), dim3(row_grid(p, L, cus, 8)), dim3(kRouterT), 0, s, p);
+  const dim3 grid(row_grid(p, L, cus, 8)), block(kRouterT);
+  if (p.E == L * V)
+    hipLaunchKernelGGL((route_kernel<L, V, K8, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((route_kernel<L, V, K8, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 template <int L, int V>
 hipError_t balance(const RouterParams& p, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL((balance_partial_kernel<L, V>), dim3(blocks), dim3(kBalanceT), 0, s, p);
+  if (p.E == L * V)
+    hipLaunchKernelGGL((balance_partial_kernel<L, V, true>), dim3(blocks), dim3(kBalanceT), 0, s, p);
+  else
+    hipLaunchKernelGGL((balance_partial_kernel<L, V, false>), dim3(blocks), dim3(kBalanceT), 0, s, p);
+  return hipGetLastError();
+}
+template <int L, int V, bool SIGMOID>
+hipError_t grad_of(const RouterParams& p, int cus, hipStream_t s) {
+  const dim3 grid(row_grid(p, L, cus, 4)), block(kRouterT);
+  if (p.E == L * V)
+    hipLaunchKernelGGL((router_grad_kernel<L, V, SIGMOID, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((router_grad_kernel<L, V, SIGMOID, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 template <int L, int V>
 hipError_t grad(const RouterParams& p, int cus, hipStream_t s) {
-  if (p.sigmoid)
-    hipLaunchKernelGGL((router_grad_kernel<L, V, true>), dim3(row_grid(p, L, cus, 4)), dim3(kRouterT), 0, s, p);
-  else
-    hipLaunchKernelGGL((router_grad_kernel<L, V, false>), dim3(row_grid(p, L, cus, 4)), dim3(kRouterT), 0, s, p);
-  return hipGetLastError();
+  return p.sigmoid ? grad_of<L, V, true>(p, cus, s) : grad_of<L, V, false>(p, cus, s);
 }
 
 }  // namespace

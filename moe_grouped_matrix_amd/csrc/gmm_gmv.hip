@@ -580,7 +580,7 @@ hipError_t launch(const GmvParams& p, int cu_count, hipStream_t s) {
   }
   const unsigned experts = p.experts + (p.weights ? 0 : 1);
   const size_t lds = (size_t)p.n * 2;
-  if ((long long)((p.N + 31) / 32) * p.experts >= 2 * cu_count)
+  if ((long long)((p.N + 31) / 32) * p.experts >= 4 * cu_count)
     hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(64 * kWaves), lds, s, p);
   else
     hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 1>), dim3(all, experts), dim3(64 * kWaves), lds, s, p);

@@ -335,7 +335,9 @@ __device__ __forceinline__ void finish_loss(const RouterParams& p, double P, lon
       all += alls[i];
     }
     const double n = tokens > 0 ? tokens : 1;
-    p.loss_out[0] = (float)((double)p.coef * p.E * dot / ((all > 0 ? all : 1) * n) + (double)p.z_coef * z2 / n);
+    // (without the term its sum is not looked at: squares of far logits overflow)
+    const double squares = p.z_coef != 0.f ? (double)p.z_coef * z2 / n : 0.0;
+    p.loss_out[0] = (float)((double)p.coef * p.E * dot / ((all > 0 ? all : 1) * n) + squares);
     p.tokens_out[0] = tokens;
   }
 }

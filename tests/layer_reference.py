@@ -14,7 +14,7 @@ INF = math.inf
 def score(z, scores):
     """Scores of one token's logits (a float64 vector with something above -inf)."""
     if scores == "sigmoid":
-        return 1 / (1 + torch.exp(-z))
+        return torch.sigmoid(z)  # 1 / (1 + exp(-z)), with a gradient of 0 where that exponential overflows
     e = torch.exp(z - z.max())
     return e / e.sum()
 
@@ -108,9 +108,9 @@ def router_grad(logits, ids, **kw):
     switched-off experts' logits left out of it."""
     z = logits.double().clone()
     off = z == -INF
-    # (an expert at -inf has score 0 and no gradient; a large negative number stands in for it, so that no 0 * inf arises)
+    # (an expert at -inf has score 0 and no gradient; a number far below every binary32 stands in for it, so that no 0 * inf arises)
     rows = counts_rows(logits, kw.get("valid"))
-    z = torch.where(off, torch.full_like(z, -1e4), z)
+    z = torch.where(off, torch.full_like(z, -1e300), z)
     z = torch.where(rows[:, None], z, torch.zeros_like(z)).requires_grad_()
     valid = rows
     kw = dict(kw, valid=valid)

@@ -191,3 +191,41 @@ def test_rows_of_a_buffer_are_left_alone():
         m.adamw([buf["p"][:n]], [buf["g"][:n]], [st["m"][:n]], [st["v"][:n]], 1, lr=0.1, copies=[cp[:n]], **kw)
         assert bool((buf["p"][n:] == 3).all()) and bool((buf["p"][:n] != 3).all()) and bool((cp[n:] == 9).all())
         assert all(bool((t.float()[n:] == 2).all()) for t in st.values()) and all(bool((t[4:] == 0.5).all()) for t in sc.values())
+
+
+def test_offsets_past_32_bits():
+    """A tensor of 2^32 + 1000 weights with eight-bit states: its first and last
+    elements step like a tensor of their own (they lie in blocks of their own)."""
+    import moe_grouped_matrix_amd as m
+    n = 2 ** 32 + 1000
+    blocks = -(-n // 256)
+    big = dict(p=torch.zeros(n, dtype=BF16, device="cuda"), g=torch.zeros(n, dtype=BF16, device="cuda"),
+               m=torch.zeros(n, dtype=torch.uint8, device="cuda").view(E4), v=torch.zeros(n, dtype=torch.uint8, device="cuda").view(E4),
+               ms=torch.ones(blocks, device="cuda"), vs=torch.ones(blocks, device="cuda"))
+    t, = _tensors([(1000,)], 8, BF16, BF16, True)
+    for lo in (0, 2 ** 32):
+        for name in ("p", "g"):
+            big[name][lo:lo + 1000] = t[name].cuda()
+        for name in ("m", "v"):
+            big[name].view(torch.uint8)[lo:lo + 1000] = t[name].view(torch.uint8).cuda()
+        for name in ("ms", "vs"):
+            big[name][lo // 256:lo // 256 + 4] = t[name].cuda()
+    m.adamw([big["p"]], [big["g"]], [big["m"]], [big["v"]], 3, exp_avg_scale=[big["ms"]], exp_avg_sq_scale=[big["vs"]], **HYPER)
+    for lo in (0, 2 ** 32):
+        d = {name: big[name][lo:lo + 1000].contiguous() for name in ("p", "m", "v")}
+        d.update({name: big[name][lo // 256:lo // 256 + 4].contiguous() for name in ("ms", "vs")})
+        _compare([t], [d], 3, **HYPER)
+
+
+def test_a_thousand_steps_of_one_tensor():
+    """The device's factors (powers by squaring in double) are the host's, for
+    steps up to the largest."""
+    import moe_grouped_matrix_amd as m
+    ts = _tensors([(300,)], 9, F32, F32, False)
+    for step in (1, 2, 3, 10, 255, 256, 1000, 123457, 2 ** 31 - 1):
+        at = torch.tensor([step], dtype=torch.int32, device="cuda")
+        a, b = _call(m, ts, step, **HYPER), _call(m, ts, at, **HYPER)
+        for name in ("p", "m", "v"):
+            assert torch.equal(a[0][name], b[0][name]), (step, name)
+    a, b = _call(m, ts, 1, **HYPER), _call(m, ts, torch.tensor([0], dtype=torch.int32, device="cuda"), **HYPER)
+    assert torch.equal(a[0]["p"], b[0]["p"])  # (a step below 1 counts as 1)

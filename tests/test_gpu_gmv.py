@@ -142,6 +142,48 @@ def test_most_slots():
     _check(_case(512, 8, 1024, 8, 32, "fp4_e2m1", 32, E8, False, False, True), "fp4_e2m1", BF16, "weighted")
 
 
+@pytest.mark.parametrize("T,k,G", [(8, 8, 9), (13, 5, 9), (1, 64, 1024), (10, 10, 300), (5, 13, 131), (5, 13, 130), (60, 4, 1000), (2, 8, 40),
+                                   (17, 1, 40), (1, 17, 40), (64, 8, 2)])
+def test_every_way_to_find_the_slots(T, k, G):
+    """Up to 64 slots, more slots than half the experts, fewer; ids that are
+    experts only in their low 32 bits are none."""
+    for weighted in (False, True):
+        x, q, ids, s, z, w = _case(T, k, G, 40, 96, "int4", 32, F32, True, weighted, weighted, G, torch.int64, 0.1)
+        ids[0, 0] = 2 ** 32 + 1
+        ids[T // 2, k - 1] = -2 ** 63
+        if weighted:
+            w[0, 0] = w[T // 2, k - 1] = math.nan
+        _check((x, q, ids, s, z, w), "int4", F32, weighted)
+    one = torch.full((T, k), G - 1)  # every slot on one expert, and none anywhere
+    x, q, _, s, z, w = _case(T, k, G, 40, 96, "uint4", 96, BF16, True, True, True, wild=0.0)
+    _check((x, q, one, s, z, w), "uint4", F32, "one")
+    _check((x, q, torch.full_like(one, -1), s, z, torch.full_like(w, math.nan)), "uint4", F32, "none")
+
+
+@pytest.mark.parametrize("K,N", [(32, 5000), (64, 1), (16384, 24), (99968, 17), (2 ** 20 - 32, 3)])
+def test_long_and_short_k(K, N):
+    for fmt, block, scale, zero in (("int4", 32, F32, False), ("uint4", K, BF16, True), ("fp4_e2m1", 32, E8, False)):
+        _check(_case(2, 2, 3, N, K, fmt, block, scale, zero, K < 1000, True, 5, wild=0.0), fmt, F32, (fmt, "weighted"))
+        _check(_case(7, 1, 1, N, K, fmt, block, scale, zero, False, False, 6, wild=0.0), fmt, BF16, fmt)
+
+
+def test_two_streams_at_once():
+    """Two weighted products that overlap in time, each with a workspace of its own."""
+    import moe_grouped_matrix_amd as m
+    cases = [_case(40, 4, 10, 1000, 512, "int4", 64, F32, False, True, True, i, wild=0.0) for i in range(2)]
+    dev = [_dev(*c) for c in cases]
+    call = lambda d, **kw: m.gmv(d[0], d[1], d[2], rhs_format="int4", rhs_scale=d[3], weights=d[5], **kw)  # noqa: E731
+    want = [call(d) for d in dev]
+    streams = [torch.cuda.Stream() for _ in dev]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[call(d, stream=st) for d, st in zip(dev, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """1024 groups of 2112 x 2048 (2.2e9 bytes of codes): the last group's product."""
     import moe_grouped_matrix_amd as m

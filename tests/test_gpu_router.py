@@ -248,3 +248,66 @@ def test_captured_and_replayed(T):
         torch.cuda.synchronize()
         for a, b in zip(made, step()):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_31_bits():
+    """2^31 - 1024 bf16 logits (4 GiB): the last token's choice, its share of the
+    loss and its gradient, all others being switched off."""
+    import moe_grouped_matrix_amd as m
+    E, k = 1024, 2
+    T = 2 ** 21 - 1
+    z = torch.full((T, E), -math.inf, dtype=BF16, device="cuda")
+    last = torch.randn(E, generator=torch.Generator().manual_seed(1)).to(BF16)
+    z[T - 1] = last.cuda()
+    ids, w = m.route(z, k)
+    want, ww, _ = ref.route(last[None], k)
+    assert torch.equal(ids[T - 1:].cpu(), want) and not bool((ids[:T - 1] != -1).any()) and not bool(w[:T - 1].any())
+    within(w[T - 1:].cpu(), ww, ww * (32 + 2 * _range(last)) * U, "weights")
+    loss, counts, tokens = m.balance_loss(z, ids, coef=0.5, z_coef=0.1)
+    lw, cw, _ = ref.balance_loss(last[None], want, coef=0.5, z_coef=0.1)
+    assert int(tokens) == 1 and torch.equal(counts.cpu(), cw)
+    assert abs(float(loss) - float(lw)) <= float(lw) * (64 + 4 * _range(last)) * U
+    dw = torch.zeros(T, k, device="cuda")
+    dw[T - 1, 0] = 1
+    got = m.router_grad(z, ids, dweights=dw)
+    gw = ref.router_grad(last[None], want, dweights=torch.tensor([[1.0, 0.0]]))
+    within(got[T - 1:].cpu(), gw, 2 * (64 + 4 * _range(last)) * U + half_step(BF16, gw), "gradient")
+    assert not bool(got[:T - 1].any())
+
+
+@pytest.mark.parametrize("E", [16, 37, 128, 200, 256, 512, 1024])
+def test_lowest_and_far_values(E):
+    """Masks of the type's lowest finite value are values like any other: chosen
+    after all others, with weight 0; sigmoid scores of both far sides."""
+    import moe_grouped_matrix_amd as m
+    for dtype in (F32, BF16):
+        low = torch.finfo(dtype).min
+        z = torch.full((3, E), low, dtype=dtype)
+        z[0, 5], z[0, 3] = 1.0, 2.0
+        z[1] = torch.linspace(-60, 60, E).to(dtype)
+        z[2, ::2] = -math.inf
+        for scores in ("softmax", "sigmoid"):
+            ids, w = (t.cpu() for t in m.route(z.cuda(), 8, scores=scores, renormalize=False))
+            want, ww, _ = ref.route(z, 8, scores, renormalize=False)
+            assert torch.equal(ids, want)
+            within(w, ww, ww * (32 + 2 * 130) * U + 2.0 ** -126, scores)
+            loss, _, tokens = m.balance_loss(z.cuda(), ids.cuda(), scores=scores)
+            assert int(tokens) == 3 and math.isfinite(float(loss))
+            g = m.router_grad(z.cuda(), ids.cuda(), dweights=torch.ones(3, 8).cuda(), scores=scores, renormalize=False).cpu()
+            gw = ref.router_grad(z, ids, dweights=torch.ones(3, 8), scores=scores, renormalize=False)
+            within(g, gw, (64 + 4 * 130) * U * 9 + half_step(dtype, gw), scores)
+
+
+def test_two_streams_at_once():
+    import moe_grouped_matrix_amd as m
+    zs = [torch.randn(3000, 100, generator=torch.Generator().manual_seed(i)).cuda() for i in range(2)]
+    ids = [m.route(z, 4)[0] for z in zs]
+    want = [m.balance_loss(z, i, z_coef=1.0) for z, i in zip(zs, ids)]
+    streams = [torch.cuda.Stream() for _ in zs]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[m.balance_loss(z, i, z_coef=1.0, stream=st) for z, i, st in zip(zs, ids, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -507,21 +507,22 @@ __global__ __launch_bounds__(64 * kWaves, 5) void gmv_kernel(GmvParams p) {
 template <Kind KIND, class S, bool WHOLE>
 __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
   constexpr int W = 16;
-  __shared__ int expert[64];
-  __shared__ int slot[64];
+  __shared__ int order[64];
   __shared__ float join[W][16];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4, n = lane & 15;
   const int n0 = blockIdx.x * 16, t = blockIdx.y;
-  // (every wave writes the same list for itself)
-  const int id = lane < p.k ? slot_expert(p, t * p.k + lane) : -1;
-  const unsigned long long live = __ballot(id >= 0);
-  if (id >= 0) {
-    const int at = __builtin_popcountll(live & ((1ull << lane) - 1));
-    expert[at] = id;
-    slot[at] = t * p.k + lane;
-  }
+  // lane j takes slot j, then lane i the i-th slot that has an expert (every wave
+  // writes the same list for itself)
+  const int own = t * p.k + (lane < p.k ? lane : 0);
+  const float own_weight = slot_weight(p, own);
+  const int own_id = lane < p.k ? slot_expert(p, own) : -1;
+  const unsigned long long live = __ballot(own_id >= 0);
+  if (own_id >= 0) order[__builtin_popcountll(live & ((1ull << lane) - 1))] = lane;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const int chunks = (p.K + 127) >> 7, all = __builtin_popcountll(live) * chunks;
+  const int count = __builtin_popcountll(live), from = lane < count ? order[lane] : 0;
+  const int id = __shfl(own_id, from, 64), slot = t * p.k + from;
+  const float scale = __shfl(own_weight, from, 64);
+  const int chunks = (p.K + 127) >> 7, all = count * chunks;
   const int lo = (int)((long long)all * w / W), hi = (int)((long long)all * (w + 1) / W);
   Sums<true> sums;
   clear(sums);
@@ -529,23 +530,29 @@ __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
   Weights d[D];
   Rows<true> xs[D];
   float weight[D];
-  auto load = [&](int i, int item) __attribute__((always_inline)) {
-    const int j = item / chunks, c = item - j * chunks;
-    const int g = __builtin_amdgcn_readfirstlane(expert[j]), s = __builtin_amdgcn_readfirstlane(slot[j]);
-    weight[i] = slot_weight(p, s);
-    load_weights<KIND, S>(d[i], p, column_of(p, g, n0 + n), c, q);
-    load_rows(xs[i], p, p.x + (long long)(p.per_slot ? s : t) * p.K, c, q);
+  int at[D];  // the chunks
+  int slot_at = lo / chunks, chunk_at = lo - slot_at * chunks;  // of the next load
+  auto load = [&](int i) __attribute__((always_inline)) {
+    const int j = __builtin_amdgcn_readfirstlane(slot_at), c = __builtin_amdgcn_readfirstlane(chunk_at);
+    weight[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), j));
+    at[i] = c;
+    load_weights<KIND, S>(d[i], p, column_of(p, __builtin_amdgcn_readlane(id, j), n0 + n), c, q);
+    load_rows(xs[i], p, p.x + (long long)(p.per_slot ? __builtin_amdgcn_readlane(slot, j) : t) * p.K, c, q);
+    if (++chunk_at == chunks) {
+      chunk_at = 0;
+      ++slot_at;
+    }
   };
 #pragma unroll
   for (int i = 0; i < D; ++i)
-    if (lo + i < hi) load(i, lo + i);
+    if (lo + i < hi) load(i);
   for (int c = lo; c < hi; c += D) {
 #pragma unroll
     for (int i = 0; i < D; ++i)
       if (c + i < hi) {
         xs[i].x[0] = __builtin_bit_cast(i32x4, ordered_x<KIND>(xs[i].x[0]));
-        use_chunk<KIND, S, WHOLE, true>(sums, d[i], xs[i], p, (c + i) % chunks, weight[i]);
-        if (c + i + D < hi) load(i, c + i + D);
+        use_chunk<KIND, S, WHOLE, true>(sums, d[i], xs[i], p, at[i], weight[i]);
+        if (c + i + D < hi) load(i);
       }
   }
   if (q == 0) join[w][n] = total<KIND, true>(sums, 0);

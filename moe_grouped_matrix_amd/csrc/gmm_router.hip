@@ -350,8 +350,6 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
   __shared__ float zsum[W];
   __shared__ int nsum[W];
   const int l = threadIdx.x & (L - 1), r = (threadIdx.x & 63) / L, w = threadIdx.x >> 6;
-  if ((int)threadIdx.x < p.E) hist[threadIdx.x] = 0;
-  __syncthreads();
   float acc[V], z2 = 0.f;
   int n = 0;
 #pragma unroll
@@ -364,6 +362,8 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
   bool next_valid = false;
   if (p.T > 0) next_valid = load_row<L, V, FULL>(next, p, t, l);  // (there may be no token at all)
   long long id = load_id(p, t, l);
+  if ((int)threadIdx.x < p.E) hist[threadIdx.x] = 0;
+  __syncthreads();
   for (; t < end; t += step) {
     Row<V> x = next;
     const bool valid = next_valid;

@@ -11,6 +11,7 @@
 
 using namespace gmmh;
 
+static_assert(gmmk::kBalanceBlocks == 256, "balance_blocks' most");
 static_assert(gmmk::kAdamBlock == GMM_ADAMW_BLOCK, "the kernels' block is the header's");
 
 namespace {

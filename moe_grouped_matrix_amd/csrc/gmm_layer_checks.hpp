@@ -52,10 +52,10 @@ inline Check check_route(const gmm_tensor* logits, const gmm_tensor* bias, const
 }
 
 // Workgroups of the balance loss's first launch, 64 tokens (16 of more than
-// 128 experts) at a time.  One workgroup alone needs no second launch and no
+// 256 experts) at a time.  One workgroup alone needs no second launch and no
 // workspace.
 inline int balance_blocks(long long T, long long E) {
-  const long long rows = E <= 128 ? 64 : 16;
+  const long long rows = E <= 256 ? 64 : 16;
   const long long b = (T + rows - 1) / rows;
   return (int)(b < 1 ? 1 : b > 256 ? 256 : b);
 }

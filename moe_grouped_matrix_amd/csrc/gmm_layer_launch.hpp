@@ -11,6 +11,7 @@ namespace gmmk {
 
 constexpr int kRouterT = 256;    // threads of the choice and the gradient: four waves
 constexpr int kBalanceT = 1024;  // of the balance loss: a thread an expert at its end
+constexpr int kBalanceBlocks = 256;  // its most workgroups
 
 // The router's tensors: T tokens, E experts, k choices.
 struct RouterParams {

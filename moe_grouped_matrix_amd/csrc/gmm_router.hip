@@ -368,12 +368,6 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
     Row<V> x = next;
     const bool valid = next_valid;
     if (t + step < end) next_valid = load_row<L, V, FULL>(next, p, t + step, l);
-    if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-    for (int j = l + L; j < p.k; j += L) {
-      id = load_id(p, t, j);
-      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-    }
-    id = load_id(p, t + step, l);
     row_state<L, V, FULL>(x, p, valid, l);
     float e[V], sum = 0.f;
 #pragma unroll
@@ -399,6 +393,12 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
       z2 = __builtin_fmaf(lse, lse, z2);
       ++n;
     }
+    if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+    for (int j = l + L; j < p.k; j += L) {
+      id = load_id(p, t, j);
+      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+    }
+    id = load_id(p, t + step, l);
   }
   // the wave's groups (they hold the same experts), then the workgroup's waves
 #pragma unroll
@@ -443,24 +443,20 @@ __global__ __launch_bounds__(kBalanceT) void balance_partial_kernel(RouterParams
 
 // Thread (slice, e) adds up every n-th workgroup's row from `slice` on; U rows
 // of both planes are in flight together.
+template <int U>
 __global__ __launch_bounds__(kBalanceT) void balance_final_kernel(RouterParams p, int B, int slices) {
-  constexpr int U = 16;
   __shared__ double sums[kBalanceT];
   __shared__ int counts[kBalanceT];
-  __shared__ double zs[64];
-  __shared__ int ns[64];
+  __shared__ double zs[kBalanceBlocks / 64];
+  __shared__ int ns[kBalanceBlocks / 64];
   const int width = kBalanceT / slices, e = threadIdx.x % width, s = threadIdx.x / width;
   const int* const cplane = reinterpret_cast<const int*>(p.work + (long long)B * p.E);
   const float* const zplane = p.work + 2ll * B * p.E;
-  if (threadIdx.x < 64) {
-    double z = 0;
-    int n = 0;
-    for (int b = threadIdx.x; b < B; b += 64) {
-      z += zplane[b];
-      n += reinterpret_cast<const int*>(zplane)[B + b];
-    }
-    zs[threadIdx.x] = z;
-    ns[threadIdx.x] = n;
+  float z = 0.f;
+  int n = 0;
+  if ((int)threadIdx.x < B) {
+    z = zplane[threadIdx.x];
+    n = reinterpret_cast<const int*>(zplane)[B + threadIdx.x];
   }
   double P = 0;
   int count = 0;
@@ -483,19 +479,28 @@ __global__ __launch_bounds__(kBalanceT) void balance_final_kernel(RouterParams p
     }
   sums[threadIdx.x] = P;
   counts[threadIdx.x] = count;
+  if (threadIdx.x < kBalanceBlocks) {  // (whole waves)
+    const double z64 = group_sum<64>((double)z);
+    n = group_sum<64>(n);
+    if ((threadIdx.x & 63) == 0) {
+      zs[threadIdx.x >> 6] = z64;
+      ns[threadIdx.x >> 6] = n;
+    }
+  }
   __syncthreads();
   double total = 0, z2 = 0;
-  int all = 0, n = 0;
+  int all = 0;
+  n = 0;
   if ((int)threadIdx.x < p.E)
     for (int i = 0; i < slices; ++i) {
       total += sums[i * width + threadIdx.x];
       all += counts[i * width + threadIdx.x];
     }
-  if (threadIdx.x == 0)
-    for (int i = 0; i < 64; ++i) {
-      z2 += zs[i];
-      n += ns[i];
-    }
+#pragma unroll
+  for (int i = 0; i < kBalanceBlocks / 64; ++i) {
+    z2 += zs[i];
+    n += ns[i];
+  }
   finish_loss(p, total, all, z2, n);
 }
 
@@ -721,7 +726,7 @@ hipError_t launch_route(const RouterParams& p, int cus, hipStream_t s) {
   const int E = p.E;
   if (p.k <= 8) {
     if (E <= 64) return route<8, 8, true>(p, cus, s);
-    if (E <= 128) return route<8, 16, true>(p, cus, s);
+    if (E <= 128) return p.T > 4096 ? route<8, 16, true>(p, cus, s) : route<16, 8, true>(p, cus, s);
     if (E <= 256) return route<16, 16, true>(p, cus, s);
     if (E <= 512) return route<64, 8, true>(p, cus, s);
     return route<64, 16, true>(p, cus, s);
@@ -739,13 +744,16 @@ hipError_t launch_balance_loss(const RouterParams& p, int blocks, hipStream_t s)
   const hipError_t e = E <= 32 ? balance<16, 2>(p, blocks, s)
                        : E <= 64 ? balance<16, 4>(p, blocks, s)
                        : E <= 128 ? balance<16, 8>(p, blocks, s)
-                       : E <= 256 ? balance<64, 4>(p, blocks, s)
+                       : E <= 256 ? balance<16, 16>(p, blocks, s)
                        : E <= 512 ? balance<64, 8>(p, blocks, s)
                                   : balance<64, 16>(p, blocks, s);
   if (e != hipSuccess || blocks == 1) return e;
   int slices = 1;
   while (slices < 32 && E * slices * 2 <= kBalanceT) slices *= 2;
-  hipLaunchKernelGGL(balance_final_kernel, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
+  if (blocks <= 4 * slices)
+    hipLaunchKernelGGL(balance_final_kernel<4>, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
+  else
+    hipLaunchKernelGGL(balance_final_kernel<16>, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
   return hipGetLastError();
 }
 
@@ -757,7 +765,7 @@ hipError_t launch_router_grad(const RouterParams& p, int cus, hipStream_t s) {
     return grad<16, 8>(p, cus, s);
   }
   if (E <= 128) return grad<64, 2>(p, cus, s);
-  if (E <= 256) return grad<64, 4>(p, cus, s);
+  if (E <= 256) return p.T > 4096 && p.k <= 16 ? grad<16, 16>(p, cus, s) : grad<64, 4>(p, cus, s);
   if (E <= 512) return grad<64, 8>(p, cus, s);
   return grad<64, 16>(p, cus, s);
 }

@@ -16,7 +16,7 @@ import warnings
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmm.so")
-EXT = os.path.join(HERE, "_moe_ext.so")  # the Python side of gmm_moe.h (host code over torch's C++ API)
+EXT = os.path.join(HERE, "_moe_ext.so")  # the Python side of gmm_moe.h and gmm_layer.h (host code over torch's C++ API)
 SOURCES = [os.path.join(CSRC, n) for n in
            ("gmm_kernels.hip", "gmm_w8a8.hip", "gmm_stream.hip", "gmm_quant.hip", "gmm_moe.hip", "gmm_mxfp4.hip", "gmm_mxw.hip",
             "gmm_router.hip", "gmm_gmv.hip", "gmm_adamw.hip", "gmm_api.cpp", "gmm_moe_api.cpp", "gmm_layer_api.cpp")]
@@ -27,8 +27,8 @@ HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-Wno-unused-command-line-argument"]
 
 # Per-source additions: the block-scaled fp8 kernel, the weight-streaming kernel
-# and the products by expert id keep their MFMA results in ordinary VGPRs, where their scale folds
-# read them.
+# and the products by expert id keep their MFMA results in ordinary VGPRs, where
+# their scale folds read them.
 EXTRA_FLAGS = {"gmm_w8a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "gmm_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "gmm_gmv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}

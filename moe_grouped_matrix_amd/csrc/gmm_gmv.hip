@@ -3,10 +3,26 @@
 //
 // What bounds it is reading every touched expert's weight once.  A workgroup
 // takes 16 NT columns of one expert and all slots that chose it (up to 16 at a
-// time); its waves share out K in contiguous chunks of 128 and join their sums
-// in LDS, so nothing is read by two waves and nothing waits for a barrier on
-// the way.  Which slots chose the r-th of the experts that were chosen at all,
-// every workgroup finds out by itself from the ids.
+// time); its four waves share out K in contiguous chunks of 128 and join their
+// sums in LDS, so nothing is read by two waves and nothing waits for a barrier on
+// the way.  Which slots chose an expert every workgroup finds out by itself from
+// the ids.
+//
+// 8 experts of 1408 x 1408 int4 for one token (8.4 MB): 4.9 us on the GPU; 32
+// tokens, top-8 of 128 (75 experts touched, 79 MB): 25-27 us, 3.1 TB/s; 64 experts
+// with a row each (67 MB) 17 us, 3.9 TB/s; dense 8192 x 4096 fp4 for four tokens
+// 7.3 us.  What is left: ids, weights and join follow one another in a workgroup
+// that reads 22 KB a tile, so that five workgroups a CU are needed to keep HBM
+// busy, and popular experts take x of 16 rows with every tile.  Tried: x of a
+// wave's chunks kept in registers and tiles taken in turn behind a bare barrier
+// (34-36 us for the 32 tokens: one tile ahead is too little in flight), two blocks
+// an operand for up to eight rows (no gain), three chunks ahead (42 us: registers),
+// eight waves a workgroup (42 us), weights loaded past the caches (47 against 39
+// us: a load takes half a line of each row).  Loads that wait for one another cost
+// most on the way: ids, scales and zero points are loaded as bits, without
+// branches, and converted when they are used (the same work with a conversion or
+// a branch behind a load: 32 against 29.5 us, and 30 against 21 for blocks of 32
+// with zero points).
 //
 // The products run on the matrix cores, x rows as the first operand of the
 // 16x16x32 product and weights as the second: that leaves the vector units
@@ -503,7 +519,10 @@ __global__ __launch_bounds__(64 * kWaves, 5) void gmv_kernel(GmvParams p) {
 // A token's weighted sum over its slots, at once: a workgroup takes 16 columns
 // of one token, its 16 waves share out the chunks of all its slots.  For a few
 // tokens, whose experts are mostly different ones, this saves the second
-// launch.
+// launch (top-8, 1408 x 704 uint4 in blocks of 32: one token 6.1 against 8.7 us, two
+// 6.8 and 10, four 12.5 and 12; 1408 x 1408 int4: 8.0 and 9.3, 8.6 and 12, 17 and
+// 13.8: hence up to 16 slots).  88 workgroups for 1408 columns is what bounds it;
+// with eight or four columns each they take 6.4 and 10.8 us.
 template <Kind KIND, class S, bool WHOLE>
 __global__ __launch_bounds__(1024) void gmv_token_kernel(GmvParams p) {
   constexpr int W = 16;
@@ -586,6 +605,10 @@ hipError_t launch(const GmvParams& p, int cu_count, hipStream_t s) {
     return hipGetLastError();
   }
   const unsigned experts = p.experts + (p.weights ? 0 : 1);
+  // 32 columns a workgroup halve what every one of them spends on ids and x, 16
+  // give twice the workgroups: from four of 32 columns a CU on, 32 (top-8 of 128,
+  // 1408 x 1408, 16 against 32: 16 slots 6.7 and 7.1 us, 32 slots 9.1 and 8.6, 256
+  // slots 34.9 and 29.5; dense 16384 x 4096 10.1 and 10.8, 32768 x 4096 17.8 and 16.4)
   const size_t lds = (size_t)p.n * 2;
   if ((long long)((p.N + 31) / 32) * p.experts >= 4 * cu_count)
     hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(64 * kWaves), lds, s, p);

@@ -239,7 +239,8 @@ typedef struct {
  * the smallest code above zero where v > 0.  A block
  * that holds an infinity or a NaN gets a NaN scale and zero codes.
  *
- * The tensors of a step must not overlap.  With step_at, a step below 1 counts
+ * The tensors of a step must not overlap, and a tensor has fewer than 2^34
+ * elements (GMM_E_UNSUPPORTED from there on).  With step_at, a step below 1 counts
  * as 1.
  */
 gmm_status gmm_adamw_run(gmm_handle* h,

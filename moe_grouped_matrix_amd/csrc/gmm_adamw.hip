@@ -32,6 +32,7 @@ namespace gmmk {
 namespace {
 
 constexpr int kAdamT = 256;
+static_assert(kAdamMost * kAdamT < (1ll << 32), "a launch has fewer than 2^32 threads");
 
 typedef short short2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));

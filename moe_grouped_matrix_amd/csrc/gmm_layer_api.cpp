@@ -13,6 +13,7 @@ using namespace gmmh;
 
 static_assert(gmmk::kBalanceBlocks == 256, "balance_blocks' most");
 static_assert(gmmk::kAdamBlock == GMM_ADAMW_BLOCK, "the kernels' block is the header's");
+static_assert(kMaxAdamElems <= gmmk::kAdamMost * gmmk::kAdamChunk, "a tensor fits a launch");
 
 namespace {
 
@@ -221,8 +222,7 @@ gmm_status gmm_adamw_run(gmm_handle* h, const gmm_adamw_item* items, int64_t cou
           const gmm_adamw_item& t = items[i];
           if (t.n == 0) continue;
           const long long chunks = (t.n + gmmk::kAdamChunk - 1) / gmmk::kAdamChunk;
-          // (a launch numbers its chunks in 31 bits)
-          if (p.count && p.first[p.count] + chunks > (1ll << 30)) {
+          if (p.count && p.first[p.count] + chunks > gmmk::kAdamMost) {
             if ((e = run()) != hipSuccess) return e;
             p.count = 0;
           }

@@ -16,7 +16,7 @@ namespace gmmh {
 constexpr long long kMaxGmvSlots = 4096;
 constexpr long long kMaxGmvCols = 1LL << 24;
 constexpr long long kMaxGmvK = 1LL << 20;
-constexpr long long kMaxAdamElems = 1LL << 40;
+constexpr long long kMaxAdamElems = 1LL << 34;
 
 // logits [T,E], ids [T,k] of the given types, valid [T].
 inline Check check_router(const gmm_tensor* logits, const gmm_tensor* ids, bool ids_written, const gmm_tensor* valid,
@@ -207,7 +207,7 @@ inline Check check_adamw(const gmm_adamw_item* items, int64_t count, const gmm_a
     const gmm_adamw_item& t = items[i];
     const std::string who = "tensor " + std::to_string(i) + ": ";
     if (t.n < 0) return invalid(who + "negative number of elements");
-    if (t.n >= kMaxAdamElems) return unsupported(who + "2^40 elements or more");
+    if (t.n >= kMaxAdamElems) return unsupported(who + "2^34 elements or more");
     if (t.n == 0) continue;
     if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return invalid(who + "null data pointer");
     if (eight != (t.exp_avg_scale != nullptr) || eight != (t.exp_avg_sq_scale != nullptr))

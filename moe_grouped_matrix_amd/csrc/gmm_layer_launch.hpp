@@ -69,6 +69,7 @@ hipError_t launch_gmv(const GmvParams& p, int cu_count, hipStream_t stream);
 constexpr int kAdamItems = 48;
 constexpr int kAdamBlock = 256;   // elements that share a scale
 constexpr int kAdamChunk = 2048;  // elements of a workgroup
+constexpr long long kAdamMost = 1 << 23;  // chunks of a launch
 constexpr long long kAdamCached = 96 << 20;  // a step that reads more streams past the caches
 struct AdamItem {
   void* p;

@@ -213,7 +213,7 @@ def test_adamw(lib):
         adam(lib, INVALID, word, items)
     adam(lib, OK, "", [item(), item(at=4000, grad=B + 4000)])
     adam(lib, OK, "", [item(grad=C + 4000)])
-    adam(lib, UNSUPPORTED, "2^40", [item(1 << 40)])
+    adam(lib, UNSUPPORTED, "2^34", [item(1 << 34)])
     adam(lib, INVALID, "need scales", [item()], state_dtype=E4M3)
     adam(lib, INVALID, "need scales", [eight(exp_avg_sq_scale=None)], state_dtype=E4M3)
     adam(lib, INVALID, "overlap", [eight(), eight(at=1 << 20, exp_avg_scale=E)], state_dtype=E4M3)

@@ -486,7 +486,8 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t elems = t.numel();
         if (role == 0) item.n = elems;
         if (elems != (role == 4 || role == 5 ? (item.n + GMM_ADAMW_BLOCK - 1) / GMM_ADAMW_BLOCK : item.n)) return none();
-        void* const at = elems ? const_cast<void*>(t.const_data_ptr()) : nullptr;
+        // (what is written becomes the tensor's own first, if it is a lazy copy)
+        void* const at = !elems ? nullptr : role == 1 ? const_cast<void*>(t.const_data_ptr()) : t.mutable_data_ptr();
         switch (role) {
           case 0: item.param = at; break;
           case 1: item.grad = at; break;

@@ -193,6 +193,15 @@ def test_rows_of_a_buffer_are_left_alone():
         assert all(bool((t.float()[n:] == 2).all()) for t in st.values()) and all(bool((t[4:] == 0.5).all()) for t in sc.values())
 
 
+def test_lazy_copies_become_their_own():
+    """A step on lazy copies leaves what they were copied from as it was."""
+    import moe_grouped_matrix_amd as m
+    old = [torch.full((300,), v, device="cuda") for v in (3.0, 0.5, 0.25)]
+    p, a, v = (torch._lazy_clone(t) for t in old)
+    m.adamw([p], [torch.ones(300, device="cuda")], [a], [v], 1, lr=0.1)
+    assert bool((p != 3).all()) and [t.unique().tolist() for t in old] == [[3.0], [0.5], [0.25]]
+
+
 def test_offsets_past_32_bits():
     """A tensor of 2^32 + 1000 weights with eight-bit states: its first and last
     elements step like a tensor of their own (they lie in blocks of their own)."""

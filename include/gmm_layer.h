@@ -71,7 +71,9 @@ extern "C" {
  * k others gets ids -1 and weights 0 behind them, and so does a token that
  * does not count.  A token with a NaN or +inf logit gets ids -1 and weights NaN.
  *
- *   bias        NULL or [E] F32.
+ *   bias        NULL or [E] F32.  An expert whose bias is -inf is never chosen
+ *               (its score still counts in the softmax); a NaN or +inf of s +
+ *               bias acts as one of a logit.
  *   expert_ids  [T,k] I32, written.
  *   weights     [T,k] F32, written.
  */
@@ -168,6 +170,8 @@ gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* byt
  * gmm_run's own (rhs_format, rhs_scale), so a larger batch goes there with the
  * same tensors.  Products and sums are fp32, rounded once.  A slot whose id is
  * outside [0,G) gives zeros: its x and weight are not read into anything.
+ * Codes times x and sums of x are added apart, so an infinity in a slot's x
+ * gives that slot NaN where the formula has an infinity (I4, U4).
  *
  *   x           [T,K] or [T,k,K] BF16.
  *   rhs         [G,N,K] I4, U4 or F4E2M1 (two to a byte), K % 32 == 0.

@@ -91,6 +91,28 @@ def test_route_with_a_bias(T, E, k, scores):
     within(w, ww, ww.abs() * (32 + 2 * _range(z)) * U + 1e-37, "weights")
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(8, 4), (128, 8), (300, 12)])
+def test_biases_that_are_not_finite(E, k, scores):
+    """-inf keeps an expert from being chosen, however few are left; NaN and
+    +inf spoil the tokens in which the expert is not switched off."""
+    import moe_grouped_matrix_amd as m
+    z = _logits(40, E, E)[0]
+    z[5, 3] = -math.inf
+    bias = torch.full((E,), -math.inf)
+    bias[[1, 3, 6]] = 0.25
+    ids, w = (t.cpu() for t in m.route(z.cuda(), k, scores=scores, bias=bias.cuda()))
+    want = [[int(e) for e in sorted((1, 3, 6), key=lambda e: -float(z[t, e])) if z[t, e] > -math.inf] for t in range(40)]
+    assert [r[r >= 0].tolist() for r in ids] == want and bool((ids[:, 3:] == -1).all()) and ids[5, 2] == -1
+    assert bool((w[ids < 0] == 0).all()) and bool((w[ids >= 0] > 0).all())
+    for far in (math.nan, math.inf):
+        bias[3] = far
+        ids, w = (t.cpu() for t in m.route(z.cuda(), k, scores=scores, bias=bias.cuda()))
+        bad = torch.arange(40) != 5
+        assert bool((ids[bad] == -1).all()) and bool(w[bad].isnan().all())
+        assert set(ids[5].tolist()) == {1, 6, -1} and bool(w[5].isfinite().all())
+
+
 def test_route_extremes():
     """Zeros of both signs tie; far logits lose to no rounding; sigmoid scores
     that underflow give weights 0; a NaN or +inf spoils its token only."""

@@ -8,9 +8,9 @@
 // so that a block's largest state is one reduction over the wave, in registers.
 //
 // It is bound by HBM: 128 x 1408 x (1408 + 704) weights in fp32 with bf16
-// gradients and copies and eight-bit states (16 bytes each, 6.1 GB) take 1110 us,
-// 5.5 TB/s, where a copy reaches 5.1; in chunks of 4096 elements 1165, of 8192
-// 1192, in a grid of eight workgroups a CU that takes chunk after chunk 1290, with
+// gradients and copies and eight-bit states (16 bytes each, 6.1 GB) take 1050 to
+// 1110 us (5.8 to 5.5 TB/s, card to card), where a copy reaches 5.1 TB/s; where they
+// took 1110, in chunks of 4096 elements 1165, of 8192 1192, in a grid of eight workgroups a CU that takes chunk after chunk 1290, with
 // one block of a wave in flight there 1300, and with a division for every code
 // and reductions through LDS 1500.  Loads past the caches help a large step
 // (1165 against 1258 us; 12 bytes of state and gradient of 15.9M weights 76 against

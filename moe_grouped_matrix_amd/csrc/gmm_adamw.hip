@@ -9,14 +9,14 @@
 //
 // It is bound by HBM: 128 x 1408 x (1408 + 704) weights in fp32 with bf16
 // gradients and copies and eight-bit states (16 bytes each, 6.1 GB) take 1050 to
-// 1110 us (5.8 to 5.5 TB/s, card to card), where a copy reaches 5.1 TB/s; where they
-// took 1110, in chunks of 4096 elements 1165, of 8192 1192, in a grid of eight workgroups a CU that takes chunk after chunk 1290, with
-// one block of a wave in flight there 1300, and with a division for every code
-// and reductions through LDS 1500.  Loads past the caches help a large step
-// (1165 against 1258 us; 12 bytes of state and gradient of 15.9M weights 76 against
-// 88) and hurt one that the last-level cache holds (4M weights: 24 against 19, 120
-// tensors of 4.4M weights: 34 against 27; about even from 64 to 128 MB read), hence
-// kAdamCached.
+// 1110 us (5.8 to 5.5 TB/s, card to card), where a copy reaches 5.1 TB/s; where
+// they took 1110, in chunks of 4096 elements 1165, of 8192 1192, in a grid of
+// eight workgroups a CU that takes chunk after chunk 1290, with one block of a
+// wave in flight there 1300, and with a division for every code and reductions
+// through LDS 1500.  Loads past the caches help a large step (1165 against 1258
+// us; 12 bytes of state and gradient of 15.9M weights 76 against 88) and hurt one
+// that the last-level cache holds (4M weights: 24 against 19, 120 tensors of 4.4M
+// weights: 34 against 27; about even from 64 to 128 MB read), hence kAdamCached.
 //
 // Every operation is rounded on its own and in a fixed order (no contraction),
 // so that the eight-bit codes, which turn on single roundings, are those of the

@@ -300,11 +300,13 @@ __device__ __forceinline__ float total(const Sums<FEW>& a, int r) {
   return a.run[0][r];
 }
 
-// The slots of the r-th expert that any slot chose: into list; returns how
-// many, and the expert (-1: fewer than r + 1 were chosen).  In which order the
-// experts are counted, and the slots listed, does not matter.  Up to 64 slots
-// each wave looks for itself: equal ids find each other by a ballot per bit of
-// the id, and an expert's first slot stands for it.
+// The slots of the r-th expert that any slot chose: into list, in their order;
+// returns how many, and the expert (-1: fewer than r + 1 were chosen).  In which
+// order the experts are counted does not matter, but that of the slots does: the
+// place in the list decides whether a slot's row is one of up to four (FEW) or of
+// sixteen, which add in different orders.  Up to 64 slots each wave looks for
+// itself: equal ids find each other by a ballot per bit of the id, and an expert's
+// first slot stands for it.
 struct Found {
   int expert, count;
 };
@@ -368,14 +370,11 @@ __device__ __forceinline__ Found find_slots(const GmvParams& p, int g, uint16_t*
 __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* list) {
   __shared__ uint8_t chosen[kMaxGroups];
   __shared__ int wave_tot[16];
-  __shared__ int expert, count;
+  __shared__ int expert;
   constexpr int T = 64 * kWaves, per = kMaxGroups / T;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   for (int g = tid; g < kMaxGroups; g += T) chosen[g] = 0;
-  if (tid == 0) {
-    expert = -1;
-    count = 0;
-  }
+  if (tid == 0) expert = -1;
   __syncthreads();
   for (int i = tid; i < p.n; i += T) {
     const int g = slot_expert(p, i);
@@ -402,12 +401,7 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
     expert = g;
   }
   __syncthreads();
-  const int g = expert;
-  if (g < 0) return {-1, 0};
-  for (int i = tid; i < p.n; i += T)
-    if (slot_expert(p, i) == g) list[atomicAdd(&count, 1)] = (uint16_t)i;
-  __syncthreads();
-  return {g, count};
+  return expert < 0 ? Found{-1, 0} : find_slots(p, expert, list);
 }
 
 // The join: every wave's sums go to LDS, join[wave][row][column], and all threads

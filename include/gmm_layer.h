@@ -246,6 +246,10 @@ typedef struct {
  * The tensors of a step must not overlap, and a tensor has fewer than 2^34
  * elements (GMM_E_UNSUPPORTED from there on).  With step_at, a step below 1 counts
  * as 1.
+ *
+ * A step of many tensors is several launches: when one of them fails
+ * (GMM_E_HIP), those before it stay queued, and the call must not be repeated
+ * as it is.
  */
 gmm_status gmm_adamw_run(gmm_handle* h,
                          const gmm_adamw_item* items,

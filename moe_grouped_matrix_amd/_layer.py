@@ -14,7 +14,8 @@ from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._binding import _DTYPE, _empty, GMM_BF16, GMM_F32, GMM_F8E4M3FN, GmmTensor, load, PACKED_FORMATS
+from ._binding import (_DTYPE, _empty, _raise, GMM_BF16, GMM_F32, GMM_F8E4M3FN, GmmTensor, handle, load,
+                       PACKED_FORMATS)
 from . import _moe
 from ._moe import _current, _device, _ID_DTYPE, _load_ext, _out, _pack, _PACKED_DTYPE, _refuse, _run
 
@@ -245,13 +246,18 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg
     weights that gmm() reads, beside float32 params).  step counts from 1; step
     (int32), lr and grad_scale (float32, a factor of the gradients) may be
     one-element device tensors, read when the step runs, as a captured graph
-    needs it.  The tensors of a role share a dtype, and none may overlap.
+    needs it.  The tensors of a role share a dtype, and none may overlap.  A refused
+    call (GmmInvalid, GmmUnsupported) changes nothing; after any other GmmError
+    some of the tensors may have taken the step.
 
     The products' weights are parameters like any other: params [G,K,N], grads
     as tgmm() returns them."""
     if stream is None and len(params):
-        if (_moe._ext or _load_ext()).adamw(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, step, lr,
-                                            *betas, eps, weight_decay, grad_scale, _current(params[0])):
+        done = (_moe._ext or _load_ext()).adamw(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, step,
+                                                lr, *betas, eps, weight_decay, grad_scale, _current(params[0]))
+        if done is not None:
+            if done is not True:  # (queued in part: not to be asked for again)
+                _raise(done, handle(params[0].device))
             return
     if len(params) == 0:
         load()

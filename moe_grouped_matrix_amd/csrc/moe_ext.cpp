@@ -6,7 +6,8 @@
 // Every function takes what is plain -- dense device tensors of fitting rank
 // and type, outputs to be made, the current stream -- and returns None for
 // anything else, a refused call included: the caller (_moe.py, _layer.py) then goes the
-// long way, which serves the other forms and says what is wrong.
+// long way, which serves the other forms and says what is wrong.  (A call that failed
+// is made again that way: it writes the same outputs.  Not so a step, see adamw.)
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -457,7 +458,8 @@ struct Column {
 };
 
 // adamw(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, step, lr, beta1, beta2, eps,
-//       weight_decay, grad_scale, stream): True, or None
+//       weight_decay, grad_scale, stream): True, None, or the status of a step that may have been queued in part (it
+//       reads what it writes, so it must not be asked for again as a refused one is)
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject* {
     Args x{a};
@@ -538,11 +540,13 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     void* const stream = x.pointer(14);
     if (!x.ok) return none();
+    gmm_status status;
     {
       Unlocked u;
-      if (g_layer.adamw(x.handle, items.data(), count, &args, stream)) x.ok = false;
+      status = g_layer.adamw(x.handle, items.data(), count, &args, stream);
     }
-    if (!x.ok) return none();
+    if (status == GMM_E_INVALID || status == GMM_E_UNSUPPORTED) return none();
+    if (status != GMM_OK) return PyLong_FromLong(status);
     Py_RETURN_TRUE;
   });
 }

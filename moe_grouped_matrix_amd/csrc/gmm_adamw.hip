@@ -271,15 +271,10 @@ __global__ __launch_bounds__(kAdamT) void adamw_kernel(AdamParams a) {
 template <class P, class G>
 hipError_t launch(const AdamParams& p, bool eight, bool stream_loads, hipStream_t stream) {
   const dim3 grid(p.first[p.count]), block(kAdamT);
-  if (eight && stream_loads)
-    hipLaunchKernelGGL((adamw_kernel<P, G, true, true>), grid, block, 0, stream, p);
-  else if (eight)
-    hipLaunchKernelGGL((adamw_kernel<P, G, true, false>), grid, block, 0, stream, p);
-  else if (stream_loads)
-    hipLaunchKernelGGL((adamw_kernel<P, G, false, true>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((adamw_kernel<P, G, false, false>), grid, block, 0, stream, p);
-  return hipGetLastError();
+  if (eight && stream_loads) return queue(adamw_kernel<P, G, true, true>, grid, block, 0, stream, p);
+  if (eight) return queue(adamw_kernel<P, G, true, false>, grid, block, 0, stream, p);
+  if (stream_loads) return queue(adamw_kernel<P, G, false, true>, grid, block, 0, stream, p);
+  return queue(adamw_kernel<P, G, false, false>, grid, block, 0, stream, p);
 }
 
 }  // namespace

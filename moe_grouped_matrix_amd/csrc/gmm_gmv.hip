@@ -594,22 +594,20 @@ __global__ __launch_bounds__(256) void gmv_join_kernel(GmvParams p) {
 template <Kind KIND, class S, bool WHOLE>
 hipError_t launch(const GmvParams& p, int cu_count, hipStream_t s) {
   const int all = (p.N + 15) / 16;
-  if (p.at_once) {
-    hipLaunchKernelGGL((gmv_token_kernel<KIND, S, WHOLE>), dim3(all, p.T), dim3(1024), 0, s, p);
-    return hipGetLastError();
-  }
+  if (p.at_once) return queue(gmv_token_kernel<KIND, S, WHOLE>, dim3(all, p.T), dim3(1024), 0, s, p);
   const unsigned experts = p.experts + (p.weights ? 0 : 1);
   // 32 columns a workgroup halve what every one of them spends on ids and x, 16
   // give twice the workgroups: from four of 32 columns a CU on, 32 (top-8 of 128,
   // 1408 x 1408, 16 against 32: 16 slots 6.7 and 7.1 us, 32 slots 9.1 and 8.6, 256
   // slots 34.9 and 29.5; dense 16384 x 4096 10.1 and 10.8, 32768 x 4096 17.8 and 16.4)
   const size_t lds = (size_t)p.n * 2;
+  hipError_t e;
   if ((long long)((p.N + 31) / 32) * p.experts >= 4 * cu_count)
-    hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 2>), dim3((p.N + 31) / 32, experts), dim3(64 * kWaves), lds, s, p);
+    e = queue(gmv_kernel<KIND, S, WHOLE, 2>, dim3((p.N + 31) / 32, experts), dim3(64 * kWaves), lds, s, p);
   else
-    hipLaunchKernelGGL((gmv_kernel<KIND, S, WHOLE, 1>), dim3(all, experts), dim3(64 * kWaves), lds, s, p);
-  if (p.weights) hipLaunchKernelGGL(gmv_join_kernel, dim3((p.N + 255) / 256, p.T), dim3(256), 0, s, p);
-  return hipGetLastError();
+    e = queue(gmv_kernel<KIND, S, WHOLE, 1>, dim3(all, experts), dim3(64 * kWaves), lds, s, p);
+  if (e != hipSuccess || !p.weights) return e;
+  return queue(gmv_join_kernel, dim3((p.N + 255) / 256, p.T), dim3(256), 0, s, p);
 }
 
 template <Kind KIND>

@@ -9,6 +9,16 @@
 
 namespace gmmk {
 
+// Queues a kernel; returns this launch's own status (hipGetLastError may hold an
+// error that another call of the thread has left, which is not for us to take).
+template <class... P>
+hipError_t queue(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t stream, const P&... args) {
+  void* at[] = {const_cast<P*>(&args)...};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, at, lds, stream);
+  if (e != hipSuccess) (void)hipGetLastError();  // (it is returned)
+  return e;
+}
+
 constexpr int kRouterT = 256;    // threads of the choice and the gradient: four waves
 constexpr int kBalanceT = 1024;  // of the balance loss: a thread an expert at its end
 constexpr int kBalanceBlocks = 256;  // its most workgroups

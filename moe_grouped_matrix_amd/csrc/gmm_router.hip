@@ -701,28 +701,18 @@ int row_grid(const RouterParams& p, int L, int cu_count, int per_cu) {
 template <int L, int V, bool K8>
 hipError_t route(const RouterParams& p, int cus, hipStream_t s) {
   const dim3 grid(row_grid(p, L, cus, 8)), block(kRouterT);
-  if (p.E == L * V)
-    hipLaunchKernelGGL((route_kernel<L, V, K8, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((route_kernel<L, V, K8, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return queue(p.E == L * V ? route_kernel<L, V, K8, true> : route_kernel<L, V, K8, false>, grid, block, 0, s, p);
 }
 template <int L, int V>
 hipError_t balance(const RouterParams& p, int blocks, hipStream_t s) {
-  if (p.E == L * V)
-    hipLaunchKernelGGL((balance_partial_kernel<L, V, true>), dim3(blocks), dim3(kBalanceT), 0, s, p);
-  else
-    hipLaunchKernelGGL((balance_partial_kernel<L, V, false>), dim3(blocks), dim3(kBalanceT), 0, s, p);
-  return hipGetLastError();
+  return queue(p.E == L * V ? balance_partial_kernel<L, V, true> : balance_partial_kernel<L, V, false>, dim3(blocks),
+               dim3(kBalanceT), 0, s, p);
 }
 template <int L, int V, bool SIGMOID>
 hipError_t grad_of(const RouterParams& p, int cus, hipStream_t s) {
   const dim3 grid(row_grid(p, L, cus, 4)), block(kRouterT);
-  if (p.E == L * V)
-    hipLaunchKernelGGL((router_grad_kernel<L, V, SIGMOID, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((router_grad_kernel<L, V, SIGMOID, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return queue(p.E == L * V ? router_grad_kernel<L, V, SIGMOID, true> : router_grad_kernel<L, V, SIGMOID, false>, grid,
+               block, 0, s, p);
 }
 template <int L, int V>
 hipError_t grad(const RouterParams& p, int cus, hipStream_t s) {
@@ -768,11 +758,8 @@ hipError_t launch_balance_loss(const RouterParams& p, int blocks, hipStream_t s)
   if (e != hipSuccess || blocks == 1) return e;
   int slices = 1;
   while (slices < 32 && E * slices * 2 <= kBalanceT) slices *= 2;
-  if (blocks <= 4 * slices)
-    hipLaunchKernelGGL(balance_final_kernel<4>, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
-  else
-    hipLaunchKernelGGL(balance_final_kernel<16>, dim3(1), dim3(kBalanceT), 0, s, p, blocks, slices);
-  return hipGetLastError();
+  return queue(blocks <= 4 * slices ? balance_final_kernel<4> : balance_final_kernel<16>, dim3(1), dim3(kBalanceT), 0, s, p,
+               blocks, slices);
 }
 
 // (16 against 64 lanes a token, 32768 tokens: 32 experts 6.0 and 17.4 us, 64: 8.2

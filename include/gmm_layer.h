@@ -170,8 +170,13 @@ gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* byt
  * gmm_run's own (rhs_format, rhs_scale), so a larger batch goes there with the
  * same tensors.  Products and sums are fp32, rounded once.  A slot whose id is
  * outside [0,G) gives zeros: its x and weight are not read into anything.
- * Codes times x and sums of x are added apart, so an infinity in a slot's x
- * gives that slot NaN where the formula has an infinity (I4, U4).
+ *
+ * With I4 and U4 codes times x and sums of x are added apart, and I4 codes as
+ * code + 8 (with or without zero points): the roundings, each 2^-24 of a partial
+ * sum, go by |scale| (|code| + |zero| + 16) |x| (U4: without the 16).  An
+ * infinity in a slot's x gives that slot NaN where the formula has an infinity,
+ * and so do finite x whose sums of (|code| + 8) |x| or (|zero| + 8) |x| pass
+ * fp32's range.
  *
  *   x           [T,K] or [T,k,K] BF16.
  *   rhs         [G,N,K] I4, U4 or F4E2M1 (two to a byte), K % 32 == 0.

@@ -14,8 +14,8 @@ from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._binding import (_DTYPE, _empty, _raise, GMM_BF16, GMM_F32, GMM_F8E4M3FN, GmmTensor, handle, load,
-                       PACKED_FORMATS)
+from ._binding import (_DTYPE, _empty, _raise, GMM_BF16, GMM_F32, GMM_F8E4M3FN, GmmError, GmmInvalid, GmmTensor,
+                       GmmUnsupported, handle, load, PACKED_FORMATS)
 from . import _moe
 from ._moe import _current, _device, _ID_DTYPE, _load_ext, _out, _pack, _PACKED_DTYPE, _refuse, _run
 
@@ -230,6 +230,11 @@ def _one(v, name: str, dtype: torch.dtype, dev: torch.device) -> Optional[int]:
     return v.data_ptr()
 
 
+def _written(tensors) -> None:
+    """What has been (or may have been) written is another version to autograd."""
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor],
           exp_avg_sq: Sequence[torch.Tensor], step: Union[int, torch.Tensor], *, lr: Union[float, torch.Tensor],
           betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
@@ -248,7 +253,9 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg
     one-element device tensors, read when the step runs, as a captured graph
     needs it.  The tensors of a role share a dtype, and none may overlap.  A refused
     call (GmmInvalid, GmmUnsupported) changes nothing; after any other GmmError
-    some of the tensors may have taken the step.
+    some of the tensors may have taken the step.  To autograd a step is an
+    in-place operation: a backward through a graph that keeps what the step
+    wrote is refused.
 
     The products' weights are parameters like any other: params [G,K,N], grads
     as tgmm() returns them."""
@@ -289,6 +296,14 @@ def adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg
         _refuse("grad_scale must be a one-element float32 device tensor")
     args = _ARGS.pack(pc, gc, mc, 0.0 if at[1] else float(lr), float(betas[0]), float(betas[1]), float(eps),
                       float(weight_decay), 0 if at[0] else int(step), at[0] or 0, at[1] or 0, at[2] or 0)
-    tensors = [*params, *grads, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()), *(copies or ())]
+    written = [*params, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ()), *(copies or ())]
+    tensors = [*written, *grads]
     tensors += [t for t in (step, lr, grad_scale) if isinstance(t, torch.Tensor)]
-    _run(load().gmm_adamw_run, dev, stream, tensors, items, len(params), args)
+    try:
+        _run(load().gmm_adamw_run, dev, stream, tensors, items, len(params), args)
+    except (GmmInvalid, GmmUnsupported):
+        raise
+    except GmmError:
+        _written(written)
+        raise
+    _written(written)

@@ -546,6 +546,16 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       status = g_layer.adamw(x.handle, items.data(), count, &args, stream);
     }
     if (status == GMM_E_INVALID || status == GMM_E_UNSUPPORTED) return none();
+    // What has been (or may have been) written is another version to autograd.
+    for (const int role : {0, 2, 3, 4, 5, 6}) {
+      if (a[role] == Py_None) continue;
+      const Column c(a[role]);
+      for (Py_ssize_t i = 0; i < c.size(); ++i) {
+        if (!THPVariable_Check(c[i])) continue;  // (a list is read as it is by now)
+        const at::Tensor& t = THPVariable_Unpack(c[i]);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+      }
+    }
     if (status != GMM_OK) return PyLong_FromLong(status);
     Py_RETURN_TRUE;
   });

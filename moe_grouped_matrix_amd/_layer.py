@@ -20,6 +20,7 @@ from . import _moe
 from ._moe import _current, _device, _ID_DTYPE, _load_ext, _out, _pack, _PACKED_DTYPE, _refuse, _run
 
 ADAMW_BLOCK = 256
+GMV_SLOTS = 4096
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _VALID_DTYPE = {t: _DTYPE[torch.int8] for t in (torch.bool, torch.uint8, torch.int8)}
@@ -184,7 +185,9 @@ def gmv(x: torch.Tensor, rhs: torch.Tensor, expert_ids: Optional[torch.Tensor] =
     k = expert_ids.shape[1] if expert_ids is not None and expert_ids.dim() == 2 else 1
     args = [_pack(x, "x", dev), _view_rhs(rhs, rhs_format, dev), _pack(rhs_scale, "rhs_scale", dev),
             _maybe(rhs_zero, "rhs_zero", dev), _maybe(expert_ids, "expert_ids", dev, _ID_DTYPE), _maybe(weights, "weights", dev)]
-    out, ov = _out(out, "out", (T, k, N) if weights is None else (T, N), out_dtype, dev, stream)
+    # (too many slots are refused by the run, whatever the output holds)
+    rows = T if T * k <= GMV_SLOTS else 0
+    out, ov = _out(out, "out", (rows, k, N) if weights is None else (rows, N), out_dtype, dev, stream)
     need = _gmv_workspace(T * k, N, weights is not None)
     work = _empty((need,), torch.uint8, dev, stream) if need else None
     _run(load().gmm_gmv_run, dev, stream, (x, rhs, rhs_scale, rhs_zero, expert_ids, weights, out), *args, ov,

@@ -178,6 +178,10 @@ gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* byt
  * and so do finite x whose sums of (|code| + 8) |x| or (|zero| + 8) |x| pass
  * fp32's range.
  *
+ * F4E2M1 weights with E8M0 scales are widened to bf16 together, as in gmm_run:
+ * exact for bytes 0 .. 252; weights past the largest bf16 (bytes 253 and 254)
+ * become infinities; byte 255 makes its block NaN.
+ *
  *   x           [T,K] or [T,k,K] BF16.
  *   rhs         [G,N,K] I4, U4 or F4E2M1 (two to a byte), K % 32 == 0.
  *   rhs_scale   [G,nb,1,N] F32 or BF16, or with F4E2M1 E8M0 (nb = K/32);

@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
 #pragma unroll
       for (int v = 0; v < V; ++v) mine[l + L * v] = 0.f;
     }
-    float s[V], soft[V], sum = 0.f, about = 0.f;
+    float slope[V], soft[V], sum = 0.f, about = 0.f;  // slope: s (1 - s), 1 - s being the sigmoid of -z in full precision
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       soft[v] = exp_of(x.z[v] - x.top);
@@ -597,14 +597,17 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
     }
     sum = group_sum<L>(sum);
     const float over_sum = over_of(sum), lse = x.top + log_of(sum);
-    float over = over_sum;  // of the sum of the scores that soft or s hold
+    float over = over_sum;  // of the sum of the scores
     if constexpr (SIGMOID) {
       float ssum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s[v] = x.z[v] > -kInf ? sigmoid(x.z[v]) : 0.f;
-        ssum += s[v];
-        about = __builtin_fmaf(a[v], s[v], about);
+        const float e = exp_of(-fabsf(x.z[v])), r = over_of(1.f + e);  // sigmoids are r and e r (1 and 0 of -inf)
+        const float score = x.z[v] >= 0.f ? r : e * r;
+        slope[v] = e * r * r;
+        asm("" : "+v"(slope[v]));  // (worked out here: two values for each, r and e r, would be kept for later)
+        ssum += score;
+        about = __builtin_fmaf(a[v], score, about);
       }
       ssum = group_sum<L>(ssum);
       over = over_scores(ssum);
@@ -664,7 +667,7 @@ __global__ __launch_bounds__(kRouterT) void router_grad_kernel(RouterParams p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if constexpr (SIGMOID)
-        d[v] = s[v] * over * (1.f - s[v]) * (a[v] - about) + soft[v] * over_sum * c;
+        d[v] = slope[v] * over * (a[v] - about) + soft[v] * over_sum * c;
       else
         d[v] = soft[v] * over_sum * (a[v] - about - off + c);
       if (p.dweights) d[v] += mine[l + L * v];

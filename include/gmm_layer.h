@@ -190,8 +190,10 @@ gmm_status gmm_gmv_workspace(int64_t slots, int64_t N, int weighted, size_t* byt
  *   expert_ids  [T,k] I32 or I64, or NULL with G = 1 (k = 1, every id 0).
  *   weights     NULL or [T,k], F32 or BF16.
  *   out         [T,k,N], with weights [T,N]; F32 or BF16.
- * Limits: T*k <= 4096 (more rows belong to gmm_run), 1 <= k <= 64,
- * G <= 1024, N < 2^24, K < 2^20 (GMM_E_UNSUPPORTED above).
+ * Limits: T*k <= 4096, 1 <= k <= 64, G <= 1024, N < 2^24, K < 2^20
+ * (GMM_E_UNSUPPORTED above).  The time grows with the rows an expert has, every
+ * sixteen reading its weight again: from some 16 rows an expert on (a single
+ * expert: 80) sorted rows and gmm_run are faster, also within the limit.
  */
 gmm_status gmm_gmv_run(gmm_handle* h,
                        const gmm_tensor* x,

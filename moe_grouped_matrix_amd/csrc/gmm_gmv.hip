@@ -1,7 +1,12 @@
 // gmm_gmv.hip -- products of a few tokens with their experts' four-bit
 // weights, by expert id (gmm_layer.h, gmm_gmv_run).
 //
-// What bounds it is reading every touched expert's weight once.  A workgroup
+// What bounds it is reading every touched expert's weight once -- for few rows an
+// expert: every sixteen rows are another pass over it, each with its loads and
+// conversions.  Sort, dispatch and the grouped product overtake it at some 16 rows
+// an expert (128 experts, top-8, 1408 x 1408 int4: 1024 slots 48 against 62 us, 2048
+// 74 and 77, 4096 138 and 79), with one expert of 8192 x 4096 at some 80 rows (64: 39.5
+// against 51, 128: 75 and 51).  A workgroup
 // takes 16 NT columns of one expert and all slots that chose it (up to 16 at a
 // time); its four waves share out K in contiguous chunks of 128 and join their
 // sums in LDS, so nothing is read by two waves and nothing waits for a barrier on
@@ -16,7 +21,8 @@
 // busy, and popular experts take x of 16 rows with every tile.  Tried: x of a
 // wave's chunks kept in registers and tiles taken in turn behind a bare barrier
 // (34-36 us for the 32 tokens: one tile ahead is too little in flight), two blocks
-// an operand for up to eight rows (no gain), three chunks ahead (42 us: registers),
+// an operand for up to eight rows (no gain), three chunks ahead (42 us: registers;
+// as it is, 32 columns with zero points spill four),
 // eight waves a workgroup (42 us), weights loaded past the caches (47 against 39
 // us: a load takes half a line of each row).  Loads that wait for one another cost
 // most on the way: ids, scales and zero points are loaded as bits, without

@@ -10,10 +10,11 @@
 //
 // 32768 tokens of 128 experts, k = 8 (16.8 MB of f32 logits; a copy of them, which
 // moves twice that, takes 6.2 us): choice 7.1 us, loss 13.1, gradient 11.1.  The
-// vector units' work bounds the choice and the gradient (5 us of each: some 70
-// and 110 instructions a wave and token), and the loss is two dependent launches
-// of 8 and 4 us.  With a wave a token and fp32 functions of the library the three
-// took 12, 109 and 17 us.
+// largest part of the choice and the gradient is the vector units' work, 84 and 98
+// instructions a token (each issued in four cycles on one of 1024 SIMDs: 4.5 and
+// 5.2 us at 2.4 GHz), and the loss is two dependent launches of 8 and 4 to 6 us.
+// With a wave a token and fp32 functions of the library the three took 12, 109 and
+// 17 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -127,7 +128,10 @@ struct Row {
 
 // Asks for the logits; what is out of range is read elsewhere in the tensor
 // (which must have a token) and put right by row_state, so that the loads need
-// no branches.  FULL: E is L V, and a lane's experts are a constant apart.
+// no branches.  FULL: E is L V, and a lane's experts are a constant apart; with
+// other numbers the bounds cost instructions and registers (32768 tokens, choice
+// and gradient: 96 experts 9.9 and 11.0 us, 128 7.4 and 11.6; 200 17.4 and 18.9,
+// 256 11.9 and 16.9; the ordered lists of 16 values a lane spill 14 to 16 there).
 template <int L, int V, bool FULL>
 __device__ __forceinline__ bool load_row(Row<V>& r, const RouterParams& p, long long t, int l) {
   const long long row = (t < p.T ? t : p.T - 1) * p.E;
@@ -728,7 +732,9 @@ hipError_t grad(const RouterParams& p, int cus, hipStream_t s) {
 // and reductions cost the same for 8 tokens a wave as for one.  32768 tokens, k =
 // 8, in us, with 8, 16 and 64 lanes: 64 experts 5.5, 9.1, 32; 128: 7.7, 9.4, 32;
 // 256: 20.5, 12.4, 32; 512 with 16 and 64: 57, 31.  A few tokens of 128 take 3.0 us
-// with 16 lanes and 3.3 with 8 (4096: 3.5 and 3.85, 8192: 4.0 and 3.9).
+// with 16 lanes and 3.3 with 8 (4096: 3.5 and 3.85, 8192: 4.0 and 3.9).  k = 10 and
+// 16: 12.6 and 17.2 us for 128 experts, 33.5 and 47.2 for 256; k = 8 with a bias:
+// 11.3 and 18.9.
 hipError_t launch_route(const RouterParams& p, int cus, hipStream_t s) {
   const int E = p.E;
   if (p.k <= 8) {

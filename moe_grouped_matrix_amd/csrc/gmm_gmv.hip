@@ -380,8 +380,11 @@ __device__ __forceinline__ Found find_slots(const GmvParams& p, int g, uint16_t*
   return {count ? g : -1, count};
 }
 
+// (fewer slots than half the experts; their experts are kept, so that the ids are
+// asked for once)
 __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* list) {
   __shared__ uint8_t chosen[kMaxGroups];
+  __shared__ int16_t experts[kMaxGroups / 2];
   __shared__ int wave_tot[16];
   __shared__ int expert;
   constexpr int T = 64 * kWaves, per = kMaxGroups / T;
@@ -391,6 +394,7 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
   __syncthreads();
   for (int i = tid; i < p.n; i += T) {
     const int g = slot_expert(p, i);
+    experts[i] = (int16_t)g;
     if (g >= 0) chosen[g] = 1;
   }
   __syncthreads();
@@ -414,7 +418,18 @@ __device__ __forceinline__ Found find_many(const GmvParams& p, int r, uint16_t* 
     expert = g;
   }
   __syncthreads();
-  return expert < 0 ? Found{-1, 0} : find_slots(p, expert, list);
+  const int g = expert;
+  if (g < 0) return {-1, 0};
+  const unsigned long long below = (1ull << lane) - 1;
+  int count = 0;
+  for (int i0 = 0; i0 < p.n; i0 += 64) {  // (every wave writes the same list)
+    const bool hit = i0 + lane < p.n && experts[i0 + lane] == g;
+    const unsigned long long here = __ballot(hit);
+    if (hit) list[count + __builtin_popcountll(here & below)] = (uint16_t)(i0 + lane);
+    count += __builtin_popcountll(here);
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return {g, count};
 }
 
 // The join: every wave's sums go to LDS, join[wave][row][column], and all threads
